@@ -13,16 +13,20 @@ import math
 
 from ._lib import DEBUG_LIB_PATH, LIB_PATH, LibraryMissing, SIGNATURES, load
 
-FA_BF16, FA_FP16, FA_FP32 = 0, 1, 2
+FA_BF16, FA_FP16, FA_FP32, FA_E4M3, FA_INT8 = range(5)
 (FA_OK, FA_ERR_NULL, FA_ERR_DTYPE, FA_ERR_HEADDIM, FA_ERR_SHAPE, FA_ERR_ALIGN, FA_ERR_CU_SEQLENS,
- FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_LAUNCH, FA_ERR_TIMEOUT, FA_ERR_BOUNDS, FA_ERR_PAGE_TABLE) = range(13)
+ FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_LAUNCH, FA_ERR_TIMEOUT, FA_ERR_BOUNDS, FA_ERR_PAGE_TABLE,
+ FA_ERR_NONFINITE, FA_ERR_SLOTS, FA_ERR_NO_PAGES) = range(16)
 FA_BUILD_DEBUG = 1
 
 __all__ = [
     "fa_fwd", "fa_fwd_prefix", "fa_bwd", "fa_bwd_masked", "fa_bwd_workspace_bytes", "attention_backward", "fa_decode_workspace_bytes", "fa_decode_splitkv", "fa_decode_splitkv_gqa", "fa_decode_splitkv_paged", "decode_paged", "fa_status_string",
     "fa_device_status", "fa_abi_version", "fa_build_flags", "fa_selftest_wait_timeout", "fa_decode_splitkv_noalloc", "FA_NOALLOC_SCRATCH_BYTES",
     "fa_decode_part_bytes", "fa_decode_splitkv_shard", "fa_decode_merge", "decode_sharded", "shard_range", "attention", "decode", "FAError", "LibraryMissing",
-    "LIB_PATH", "DEBUG_LIB_PATH", "FA_BF16", "FA_FP16", "FA_FP32", "FA_BUILD_DEBUG",
+    "LIB_PATH", "DEBUG_LIB_PATH", "FA_BF16", "FA_FP16", "FA_FP32", "FA_E4M3", "FA_INT8", "FA_BUILD_DEBUG",
+    "fa_kv8_append", "fa_kv8_attend", "fa_kv8_attend_workspace_bytes", "append_kv8", "attend_kv8", "new_kv8_cache",
+    "fa_pages_workspace_bytes", "fa_pages_extend", "fa_pages_fork", "fa_pages_free", "fa_pages_compact", "fa_pages_copy",
+    "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_pages",
 ]
 
 
@@ -374,3 +378,8 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens_k=None, scale=None, n
 
 
 from .sharded import decode_sharded, shard_range  # noqa: E402  (key-sharded decode over ranks)
+from .kv8 import (  # noqa: E402  (paged cache held in 8 bits)
+    append_kv8, attend_kv8, fa_kv8_append, fa_kv8_attend, fa_kv8_attend_workspace_bytes, new_kv8_cache)
+from .pages import (  # noqa: E402  (pages of a cache)
+    compact_pages, copy_pages, extend_pages, fa_pages_compact, fa_pages_copy, fa_pages_extend, fa_pages_fork, fa_pages_free,
+    fa_pages_workspace_bytes, fork_pages, free_pages)

@@ -33,6 +33,15 @@ SIGNATURES = {
     "fa_decode_part_bytes": (_Z, [_I, _I, _I]),
     "fa_decode_splitkv_shard": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _Z, _P, _I]),
     "fa_decode_merge": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _I]),
+    "fa_kv8_append": (_I, [_P] * 9 + [_I] * 7 + [_P, _I, _I]),
+    "fa_kv8_attend_workspace_bytes": (_Z, [_I] * 5),
+    "fa_kv8_attend": (_I, [_P] * 8 + [_I] * 8 + [_F, _P, _P, _Z, _P, _I, _I, _I]),
+    "fa_pages_workspace_bytes": (_Z, [_I] * 3),
+    "fa_pages_extend": (_I, [_P] * 5 + [_I] * 5 + [_P, _Z, _P]),
+    "fa_pages_fork": (_I, [_P] * 5 + [_I] * 5 + [_P, _P, _I, _P, _Z, _P]),
+    "fa_pages_free": (_I, [_P] * 4 + [_I] * 5 + [_P]),
+    "fa_pages_compact": (_I, [_P] * 7 + [_I] * 4 + [_P, _P, _I, _P, _Z, _P]),
+    "fa_pages_copy": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _Z, _P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_device_status": (_I, [ctypes.POINTER(_I), _I]),
     "fa_abi_version": (_I, []),

@@ -120,6 +120,9 @@ const char* fa_status_string(int status) {
     case FA_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
     case FA_ERR_BOUNDS: return "an index check of the debug build caught an access outside its buffer";
     case FA_ERR_PAGE_TABLE: return "a block-table entry of the paged cache names no page of the pool";
+    case FA_ERR_NONFINITE: return "a row appended to an 8-bit cache holds an infinity or NaN";
+    case FA_ERR_SLOTS: return "a list of slots or pages is out of range, names one twice, or reads and writes the same one";
+    case FA_ERR_NO_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

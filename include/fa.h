@@ -43,7 +43,10 @@ extern "C" {
 struct CUstream_st;                     /* the same type as cudaStream_t */
 typedef struct CUstream_st* fa_stream_t;
 
-typedef enum { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype;
+typedef enum {
+  FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2,
+  FA_E4M3 = 3, FA_INT8 = 4  /* codes of an 8-bit cache (fa_kv8_*) only */
+} fa_dtype;
 
 typedef enum {
   FA_OK = 0,
@@ -59,8 +62,12 @@ typedef enum {
   FA_ERR_TIMEOUT = 10,    /* a bounded wait inside a kernel ran out (device-detected)         */
   FA_ERR_BOUNDS = 11,     /* debug builds only: an index check caught an access outside its
                              buffer (device-detected; the access was skipped)                  */
-  FA_ERR_PAGE_TABLE = 12  /* a paged-cache block-table entry names no pool page
+  FA_ERR_PAGE_TABLE = 12, /* a paged-cache block-table entry names no pool page
                              (device-detected; see fa_decode_splitkv_paged)                     */
+  FA_ERR_NONFINITE = 13,  /* a row given to fa_kv8_append holds an infinity or NaN (device-detected) */
+  FA_ERR_SLOTS = 14,      /* a list of slots or pages is out of range, names one twice, or both reads
+                             and writes one (device-detected; see fa_pages_*)                    */
+  FA_ERR_NO_PAGES = 15    /* fewer free pages than a request needs (device-detected)             */
 } fa_status;
 
 /*
@@ -243,6 +250,165 @@ int fa_decode_splitkv_paged(const void* q, const void* k_pages, const void* v_pa
                             int pages_per_seq, int D, float scale, int num_splits, const int* seqlens_k,
                             void* workspace, size_t workspace_bytes, fa_stream_t stream, int in_dtype,
                             int o_dtype);
+
+/*
+ * ---- Paged cache held in 8 bits ----------------------------------------------------------------
+ *
+ * The pages ask whether a backend supports the cache layout ("Was FlashAttention bei
+ * Transformer-Inference verändert") without fixing one; decode is bound by reading the cache, so a
+ * cache of half the bytes is read in half the time.  Four pools, indexed by page:
+ *   k_pages, v_pages    [num_pages, Hkv, page_size, D] codes of one byte: FA_E4M3 (sign, 4 exponent and
+ *                       3 mantissa bits, largest value 448, no infinity) or FA_INT8 (-127 .. 127);
+ *   k_scales, v_scales  [num_pages, Hkv, page_size / 16] fp32: one scale per 16 tokens and head.
+ * The value of a code is code * scale.  (Heads come before rows, unlike the 16-bit pools of
+ * fa_decode_splitkv_paged: the rows of one head in one page are one contiguous run.)  Block tables and
+ * page sizes are those of fa_decode_splitkv_paged: block_table int32 [B, pages_per_seq], entry (b, i)
+ * the page of keys [i * page_size, (i + 1) * page_size) of item b; page_size a power of two, 16 to
+ * 65536; num_pages * page_size * Hkv below 2^40, pages_per_seq * page_size at most 2^30,
+ * B * pages_per_seq below 2^31; B and Hkv (and Hq) at most 65535.  Pools and 16-bit tensors are
+ * 16-byte aligned, scales, tables and lengths 4-byte aligned.
+ * Errors of both entry points: FA_ERR_NULL, FA_ERR_DTYPE (kv_dtype not FA_E4M3 / FA_INT8, or a 16-bit
+ * type as fa_fwd), FA_ERR_HEADDIM, FA_ERR_SHAPE, FA_ERR_ALIGN, FA_ERR_DEVICE, FA_ERR_LAUNCH; on the
+ * device FA_ERR_CU_SEQLENS (a length outside its range: the item is skipped by the append, and has no
+ * keys for the attention) and FA_ERR_PAGE_TABLE (a table entry that is needed and names no page of the
+ * pool: nothing outside the pool is touched, the block is not written, and an item that reads it has
+ * no meaningful O and LSE).
+ */
+
+/*
+ * fa_kv8_append -- quantise new K and V rows into the cache.
+ *
+ * k, v [B, Nt, Hkv, D] of in_dtype.  seqlens_k: device int32[B], the lengths with the new rows
+ * included (those the attention of the same step takes); new_lens: device int32[B] or NULL (Nt for
+ * every item): the first new_lens[b] of item b's Nt rows become its keys seqlens_k[b] - new_lens[b] to
+ * seqlens_k[b] - 1, the others are ignored.  0 <= new_lens[b] <= Nt, new_lens[b] <= seqlens_k[b] <=
+ * pages_per_seq * page_size.
+ * A block is 16 consecutive keys (from a multiple of 16) of one head.  Of each block that gets new rows:
+ * a = the largest magnitude of its new finite values; scale = the smallest power of two s >= 2^-126
+ * with a <= 448 s (FA_E4M3) or a <= 127 s (FA_INT8), or the scale its older rows have, if that is larger;
+ * older rows' codes c become rn(c * old / scale) if the scale grew; a new value's code is rn(x / scale)
+ * (round to nearest even).  An infinity is stored as the largest code of its sign and a NaN as 0, and
+ * the device status becomes FA_ERR_NONFINITE.  Rows behind the new ones keep their bytes.  Two items of
+ * one call must not write the same block.  One kernel; needs no workspace.
+ */
+int fa_kv8_append(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                  const int* block_table, const int* seqlens_k, const int* new_lens, int B, int Nt, int Hkv,
+                  int num_pages, int page_size, int pages_per_seq, int D, fa_stream_t stream, int in_dtype,
+                  int kv_dtype);
+
+/*
+ * fa_kv8_attend_workspace_bytes -- size of the scratch buffer fa_kv8_attend needs.  Returns 0 for
+ * invalid arguments.
+ */
+size_t fa_kv8_attend_workspace_bytes(int B, int Nq, int Hq, int Hkv, int D);
+
+/*
+ * fa_kv8_attend -- attention of the newest Nq tokens of each sequence over its 8-bit cache.
+ *
+ * Nq = 1 is decode; a few tokens verify a draft; many are a chunk of a prompt behind a cached prefix.
+ * q [B, Nq, Hq, D] of in_dtype; o the same shape, of o_dtype (in_dtype or FA_FP32); lse [B, Hq, Nq] fp32.
+ * Hq must be a multiple of Hkv; query head h reads KV head h / (Hq / Hkv).  seqlens_k: device int32[B] or
+ * NULL (pages_per_seq * page_size for every item): the queries are item b's last Nq keys' tokens, so
+ * query i sees key j iff j <= seqlens_k[b] - Nq + i (the causal mask of fa_fwd, aligned at the
+ * bottom-right corner).  A query that sees no key (a length below Nq, or 0) gets O = 0, LSE = -inf: in a
+ * batch of chunks of unlike lengths the shorter ones are padded in front.  Rows of a page at or behind
+ * seqlens_k[b] may hold anything, NaN codes included.  Among the keys below it a NaN code makes O
+ * (V) or O and LSE (K) of any query of that item and head unspecified, masked from it or not
+ * (fa_kv8_append writes none).  Scales are finite and not negative.
+ * Both products run on fp16 operands, in which every code is exact, with fp32 accumulation; the softmax
+ * weights are rounded to fp16, relative to the largest contribution to O; nothing else is rounded below
+ * fp32 before O.  Nq * Hq * B and B * Hkv * Nq below 2^31; Nq at most 2^24.
+ * workspace: at least fa_kv8_attend_workspace_bytes(B, Nq, Hq, Hkv, D) bytes, 16-byte aligned, owned by the
+ * caller; its contents on entry are irrelevant; calls that may overlap need one each.
+ * Errors as above, plus FA_ERR_WORKSPACE.
+ */
+int fa_kv8_attend(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                  const float* v_scales, const int* block_table, void* o, float* lse, int B, int Nq, int Hq,
+                  int Hkv, int num_pages, int page_size, int pages_per_seq, int D, float scale,
+                  const int* seqlens_k, void* workspace, size_t workspace_bytes, fa_stream_t stream,
+                  int in_dtype, int kv_dtype, int o_dtype);
+
+/*
+ * ---- Pages of a cache -------------------------------------------------------------------------
+ *
+ * What keeps the block tables of a paged cache (8-bit or 16-bit), without the host in between.  State,
+ * device int32, 4-byte aligned: block_table [S, pages_per_seq] (row s: the pages of slot s in key
+ * order), seqlens [S] (keys of each slot; 0 = an empty slot), refcount [num_pages] (how many slots hold
+ * the page; 0 = free).  A caller starts with zeroed seqlens and refcount; the first
+ * ceil(seqlens[s] / page_size) entries of a row are in use, the others mean nothing.
+ * Pages are handed out from the lowest free one on, in the order of the request's list, so the outcome
+ * depends on the inputs alone.  A request of fa_pages_extend, _fork or _copy is met as a whole or, when the
+ * device finds it faulty, changes nothing and sets the device status.
+ * Slot, page and length lists (slots, add, src, dst) are device int32 of n entries, 4-byte aligned.
+ * page_size as above; S, n, num_pages, pages_per_seq >= 1; S * pages_per_seq below 2^31,
+ * pages_per_seq * page_size at most 2^30, n at most 2^20, num_pages and S at most 2^28.
+ * Pools: `pools` is a HOST array of n_pools device pointers, `page_bytes` a HOST array of the bytes one
+ * page takes in each (both are read before the call returns): page p of pool i is the page_bytes[i]
+ * bytes at pools[i] + p * page_bytes[i].  Pointers 4-byte aligned, page_bytes a multiple of 4 (16 for
+ * both is faster), n_pools at most 65536.  A page has the same place in every pool, so one call serves
+ * the K and V (and scale) pools of all layers.
+ * workspace: at least fa_pages_workspace_bytes(n, S, num_pages) bytes, 16-byte aligned; its contents on
+ * entry are irrelevant; calls that may overlap need one each.  Calls on one state must be ordered.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_ALIGN, FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_LAUNCH.
+ */
+
+/* fa_pages_workspace_bytes -- size of the scratch buffer of the calls below (for fa_pages_compact n = 1,
+ * for fa_pages_copy num_pages = the larger pool's).  Returns 0 for invalid arguments. */
+size_t fa_pages_workspace_bytes(int n, int S, int num_pages);
+
+/*
+ * fa_pages_extend -- lengthen slots by add[i] keys each and give them the pages that takes.
+ * slots: the slots to lengthen, each at most once, or NULL (slots 0 .. n - 1; n <= S).  add[i] >= 0 and
+ * the new length at most pages_per_seq * page_size.  seqlens, block_table and refcount are updated.  The
+ * last page of a slot must not be shared if it is partial (fa_pages_fork sees to that).
+ * On the device: FA_ERR_SLOTS, FA_ERR_CU_SEQLENS, FA_ERR_NO_PAGES (nothing changed).
+ */
+int fa_pages_extend(int* block_table, int* seqlens, int* refcount, const int* slots, const int* add, int n,
+                    int S, int pages_per_seq, int num_pages, int page_size, void* workspace,
+                    size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_pages_fork -- make slot dst[i] a copy of slot src[i]: full pages are shared (their counts grow), a
+ * last partial page is copied in every pool to a free page, so that both may go on on their own.
+ * A source may be named several times; the destinations are distinct, empty (length 0) and no sources.
+ * On the device: FA_ERR_SLOTS, FA_ERR_CU_SEQLENS, FA_ERR_NO_PAGES, FA_ERR_PAGE_TABLE for a partial page
+ * outside the pool (nothing changed), and FA_ERR_PAGE_TABLE for a full page outside it (not counted).
+ */
+int fa_pages_fork(int* block_table, int* seqlens, int* refcount, const int* src, const int* dst, int n, int S,
+                  int pages_per_seq, int num_pages, int page_size, void* const* pools, const size_t* page_bytes,
+                  int n_pools, void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_pages_free -- empty slots: their pages' counts fall by one, their used table entries become -1,
+ * their lengths 0.  An empty slot, or a slot named again, is left as it is.  On the device: FA_ERR_SLOTS,
+ * FA_ERR_CU_SEQLENS, FA_ERR_PAGE_TABLE (an entry outside the pool, or of a page nobody holds).
+ */
+int fa_pages_free(int* block_table, int* seqlens, int* refcount, const int* slots, int n, int S,
+                  int pages_per_seq, int num_pages, int page_size, fa_stream_t stream);
+
+/*
+ * fa_pages_compact -- move the live pages (refcount > 0) to the front of the pools: with n_live of them,
+ * the j-th live page at or behind place n_live moves to the j-th free place before it, in every pool; the
+ * others stay.  remap [num_pages]: the new place of each live page, -1 for free ones.  n_live [1].
+ * block_table_out and refcount_out receive the state of the new places (entries not in use are copied);
+ * they may be block_table and refcount themselves, and must not overlap them otherwise.
+ * On the device: FA_ERR_PAGE_TABLE (an entry in use that names no live page becomes -1),
+ * FA_ERR_CU_SEQLENS (that row is copied as it is).
+ */
+int fa_pages_compact(const int* block_table, const int* seqlens, const int* refcount, int* block_table_out,
+                     int* refcount_out, int* remap, int* n_live, int S, int pages_per_seq, int num_pages,
+                     int page_size, void* const* pools, const size_t* page_bytes, int n_pools, void* workspace,
+                     size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_pages_copy -- copy page src[i] of each pool src_pools[k] to page dst[i] of dst_pools[k] (which may be
+ * the same pool): src_num_pages and dst_num_pages pages, same page_bytes.  Destinations are distinct; if
+ * any pool is on both sides, none is also a source.  On the device: FA_ERR_PAGE_TABLE (an index outside
+ * its pool), FA_ERR_SLOTS (nothing changed).  Pools must not overlap unless they are the same.
+ */
+int fa_pages_copy(const void* const* src_pools, void* const* dst_pools, const size_t* page_bytes, int n_pools,
+                  const int* src, const int* dst, int n, int src_num_pages, int dst_num_pages, void* workspace,
+                  size_t workspace_bytes, fa_stream_t stream);
 
 /*
  * fa_decode_part_bytes -- size of one key shard's partial decode result (see

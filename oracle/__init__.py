@@ -16,7 +16,10 @@ Modules:
   brute      -- scalar pure-Python (math.fsum) evaluation for tiny inputs.
   backward   -- dQ, dK, dV: the derivative of the forward definition for an upstream gradient dO
                 (whole head, dense, packed varlen, and at sampled rows of long heads).
+  kv8        -- the paged 8-bit cache: codes, the append's quantisation, attention over the values.
+  pages      -- the operations on a cache's pages (extend, fork, free, compact), one after another.
 """
+from . import kv8, pages
 from .attention import (attention_head, attention_dense, attention_varlen, attention_rows,
                         attention_decode, attention_decode_gqa, attention_decode_shard,
                         attention_decode_paged, padded_key_mask_attention)
@@ -32,5 +35,5 @@ __all__ = [
     "padded_key_mask_attention", "tiled_online_attention", "group_stats", "merge_groups",
     "softmax_by_groups", "split_kv_partials", "combine_partials", "brute_attention_head",
     "attention_head_backward", "attention_dense_backward", "attention_varlen_backward",
-    "attention_rows_backward",
+    "attention_rows_backward", "kv8", "pages",
 ]
