@@ -12,15 +12,23 @@
 // significant bits) relative to the largest contribution whatever the scales are, and nothing
 // overflows.  At the end O * 2^(mo - m) / l.  Both maxima are raised lazily (by more than 2^8 only).
 //
-// Rows: the G = Hq / Hkv query heads of a KV head times the Nq tokens, token-major, in tiles of 16 (the M
-// of a warp MMA).  CTA = (row tile, KV head; split of the keys; sequence), four warps.  Warp w takes every
+// Rows: the G = Hq / Hkv query heads of a KV head times the Nq tokens, token-major, in tiles of 8, 16, 24 or 32:
+// keys are the M of the warp MMAs and rows their N, so that few rows waste little of the tensor pipe (a
+// 16-row M took 275 of its cycles per block where 8 rows take 138):
+//   S^T [16 keys x 8 rows]   = K [16 keys x D] Q^T,   O^T [D x 8 rows] += V^T [D x 16 keys] W^T [16 keys x 8 rows];
+// the weights go from the accumulator's layout to the operand's with a movmatrix.
+// Work is cut evenly over the CTAs (two to four per SM), whatever the lengths are: the
+// granules (64 keys) of all units (sequence, row tile, KV head) are numbered through, CTA c takes the
+// c-th equal share, which may begin and end inside a unit, and finds its place with a scan over the
+// lengths.  A unit that lies in one share is written at once; the pieces of the others go to the
+// workspace (at most two per CTA) and are merged in order by a second kernel.  Warp w of the four takes every
 // fourth block of 16 keys: a block has one scale per pool and lies in one page, so a warp needs nothing
-// from the others until the end.  It streams its blocks (16 x D bytes of K and of V, contiguous in a
+// from the others until the end of a unit.  It streams its blocks (16 x D bytes of K and of V, contiguous in a
 // page) through a ring of its own in shared memory with 16-byte cp.async, keys past the end filled with
 // zeros, and reads them back as 16-byte (K) and 16- or 8-byte (V) pieces of a row: which k slot of an
 // MMA a value takes is free as long as both operands agree, so no transposition is needed but of the
 // byte pairs of V (two PRMT per eight codes).  The ring's 16-byte chunks are swizzled so that both reads
-// are free of bank conflicts.  Warps and splits are merged by their (m, l, mo, O).
+// are free of bank conflicts.  Warps and pieces are merged by their (m, l, mo, O).
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -31,14 +39,14 @@
 namespace fa {
 namespace {
 
-constexpr int kRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 6;
 constexpr float kLazy = 8.f;  // log2 units by which a maximum may be exceeded before it is raised
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
-constexpr int kMaxSplits = 64;
-constexpr int kSplitKeys = 256;  // a split covers at least this many keys
+constexpr int kSms = 148;
+constexpr int kGranule = 64;      // keys: one block of 16 for each warp
+constexpr int kMinGranules = 4;   // of a share: shorter ones cost more to merge than to read
+constexpr int kShortKeys = 512;   // tables up to this many keys: a granule is a whole unit, and nothing is merged
 
 struct AttParams {
   const void* q;
@@ -50,22 +58,30 @@ struct AttParams {
   const int* seqlens;
   void* o;
   float* lse;
-  float* ws_o;  // [B * Nq * Hq, S, D]
-  float* ws_l;  // [B * Nq * Hq, S]
-  int B, Nq, Hq, Hkv, group, tiles, S;
+  float* ws_o;  // [2 * shares, rows of a tile, D]: pieces of units
+  float* ws_l;  // [2 * shares, rows of a tile]
+  int B, Nq, Hq, Hkv, group, tiles;
+  int granule;  // keys
   int num_pages, page_shift, pps;
   float scale_log2;
   int* status;
 };
 
-template <int D>
+// CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.
+template <int NG>
+constexpr int kPerSm = NG == 1 ? 4 : NG == 2 ? 3 : 2;
+
+template <int D, int NG>
 struct Ring {
-  static constexpr int kBlock = kKv8Block * D;    // bytes of 16 keys of K or V
+  static constexpr int kRows = 8 * NG;
+  static constexpr int kBlock = kKv8Block * D;  // bytes of 16 keys of K or V
   static constexpr int kStage = 2 * kBlock;
+  static constexpr int kRoom = (227 * 1024 / kPerSm<NG> - 2048) / kWarps - 128;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
   static constexpr int kWarp = kStages * kStage + 128;  // the stages, then (ks, vs) of each, 16 bytes apart
   static constexpr int kMerge = kWarps * kRows * (D + 3) * 4;
   static constexpr int kSmem = kWarps * kWarp > kMerge ? kWarps * kWarp : kMerge;
-  static_assert(kStages * 16 <= 128, "scales of the stages");
+  static_assert(kStages >= 3 && kStages * 16 <= 128, "stages, and their scales");
 };
 
 // Byte offset of 16-byte chunk ch of row r of a 16 x D block.  D = 128: a row is one 128-byte line; rows
@@ -77,35 +93,59 @@ __device__ __forceinline__ uint32_t ring_off(int r, int ch) {
   else return (r >> 1) * 128 + ((((r & 1) * 4 + ch) ^ (2 * ((r >> 1) & 3))) << 4);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
+// Float of row r, column d in the merge buffer: 16-byte chunks swizzled so that the eight lanes that store
+// at once (two columns D / 8 apart, rows 2t) do not share banks.
+template <int D>
+__device__ __forceinline__ int merge_at(int r, int d) {
+  const int ch = d >> 2, t = (r >> 1) & 3;
+  return r * D + ((ch ^ (D == 128 ? t : (t & 1) | ((t >> 1) << 2))) << 2) + (d & 3);
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool full) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool full) {
+__device__ __forceinline__ void cp4_or_zero(uint32_t dst, const void* src, bool full) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(full ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Two codes (the low 16 bits) as two fp16 values.
+// Four codes as fp16 pairs: e4m3 codes (0, 1) and (2, 3) of the word by the hardware's conversion (2.9 clocks
+// per warp and pair), int8 codes (0, 2) and (1, 3): code + 128 in the mantissa of 1024, less 1152, all exact.
 template <bool kInt8>
-__device__ __forceinline__ uint32_t half2_of(uint32_t two) {
-  uint32_t h;
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (kInt8) {
-    // code + 128 in the mantissa of 1024: 1024 + (code + 128) - 1152, all exact
-    h = __byte_perm(two ^ 0x8080u, 0x64646464u, 0x4140);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
-    h = *reinterpret_cast<const uint32_t*>(&x);
+    lo = (w & 0x00FF00FFu) ^ 0x64806480u;
+    hi = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&lo), off), y = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
   } else {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
   }
-  return h;
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// Bytes 2i, 2i + 1 of two words so that halves_of gives (x, y) pairs of byte 2i (lo) and 2i + 1 (hi).
+template <bool kInt8, int i>
+__device__ __forceinline__ uint32_t pair_bytes(uint32_t x, uint32_t y) {
+  return __byte_perm(x, y, kInt8 ? (i ? 0x7632 : 0x5410) : (i ? 0x7362 : 0x5140));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -128,358 +168,576 @@ __device__ __forceinline__ void store2(void* o, size_t at, float a, float b, boo
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o) + at) = pack2<kFp16>(a, b);
 }
 
-template <bool kFp16, bool kInt8, int D>
-__global__ void __launch_bounds__(kThreads, 2) kv8_attend_kernel(const AttParams p, const int o_fp32) {
-  using R = Ring<D>;
-  constexpr int LD = D / 64;  // 16-byte pieces of a K row per lane
-  constexpr int NT = D / 8;   // 8-column tiles of O
-  extern __shared__ __align__(128) uint8_t smem[];
+// Keys of batch item b (0 for a length outside its range).
+__device__ __forceinline__ int keys_of(const AttParams& p, int b) {
+  const int cap = p.pps << p.page_shift;
+  if (!p.seqlens) return cap;
+  const int len = __ldg(p.seqlens + b);
+  return len < 0 || len > cap ? 0 : len;
+}
+
+// Keys that a row sees (rows of a token see the same ones), and granules of a row tile.
+__device__ __forceinline__ int row_limit(const AttParams& p, int len, int row) { return max(0, len - p.Nq + row / p.group + 1); }
+template <int kRows>
+__device__ __forceinline__ int tile_keys(const AttParams& p, int len, int tile) {
+  return row_limit(p, len, min(p.Nq * p.group, (tile + 1) * kRows) - 1);
+}
+template <int kRows>
+__device__ __forceinline__ int tile_granules(const AttParams& p, int len, int tile) {
+  return (tile_keys<kRows>(p, len, tile) + p.granule - 1) / p.granule;
+}
+template <int kRows>
+__device__ __forceinline__ long long item_granules(const AttParams& p, int b) {
+  const int len = keys_of(p, b);
+  long long n = 0;
+  for (int i = 0; i < p.tiles; ++i) n += tile_granules<kRows>(p, len, i);
+  return n * p.Hkv;
+}
+
+// Where a share begins: item b, granule `off` among the item's.
+struct Place {
+  long long total;  // granules of all items
+  long long off;
+  int b;
+};
+
+struct ScanMem {
+  long long sums[kWarps];
+  long long off;
+  int b;
+};
+
+// Number of shares of `total` granules, and the first granule of share c.
+__device__ __forceinline__ int shares_of(const AttParams& p, long long total, int grid) {
+  const int least = p.granule == kGranule ? kMinGranules : 1;
+  return static_cast<int>(min(static_cast<long long>(grid), (total + least - 1) / least));
+}
+__device__ __forceinline__ long long share_begin(long long total, int shares, int c) { return total * c / shares; }
+
+// The place of the first granule of share c: a scan of the items' granules, a CTA's worth at a time, once
+// for the total and (with more items than threads) once to find the place.  Collective.
+template <int kRows>
+__device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c, ScanMem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int tile = blockIdx.x % p.tiles, hk = blockIdx.x / p.tiles, split = blockIdx.y, b = blockIdx.z;
-  const int rows = p.Nq * p.group, row0 = tile * kRows;
-
-  const long long cap = static_cast<long long>(p.pps) << p.page_shift;
-  int len = static_cast<int>(cap);
-  if (p.seqlens) {
-    len = __ldg(p.seqlens + b);
-    if (len < 0 || len > cap) {
-      if (tid == 0 && split == 0 && blockIdx.x == 0) record_status(p.status, kStatusCuSeqlens);
-      len = 0;
-    }
-  }
-  // keys that a row of token i sees: len - Nq + i + 1; of the tile: those its last and its first row see
-  auto limit = [&](int row) { return max(0, len - p.Nq + row / p.group + 1); };
-  const int tile_end = limit(min(rows, row0 + kRows) - 1), tile_all = limit(row0);
-  const int per = (max((tile_end + p.S - 1) / p.S, kSplitKeys) + 63) & ~63;
-  const int lo = static_cast<int>(min(static_cast<long long>(tile_end), static_cast<long long>(split) * per));
-  const int hi = min(tile_end, lo + per);
-  int lim[2];
+  Place r;
+  long long mine = 0, sum = 0;
+  for (int b = tid; b < p.B; b += kThreads) sum += (mine = item_granules<kRows>(p, b));
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = row0 + g + 8 * r;
-    lim[r] = row < rows ? limit(row) : 0;
-  }
-
-  // queries: A operand of row g (and g + 8); piece i of 16 values from d = 16 (t + 4 i)
-  uint32_t qa[LD][4][4];
-  float qs[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = row0 + g + 8 * r;
-    const bool in = row < rows;
-    const size_t at = ((static_cast<size_t>(b) * p.Nq + row / p.group) * p.Hq + hk * p.group + row % p.group) * D;
-    uint32_t u[LD][8];
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + 16 * (t + 4 * i));
-      const bool ok = in && idx_ok(p.status, at + 16 * (t + 4 * i), 16, static_cast<long long>(p.B) * p.Nq * p.Hq * D);
-      const uint4 a = ok ? __ldg(src) : make_uint4(0, 0, 0, 0), c = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-      u[i][0] = a.x; u[i][1] = a.y; u[i][2] = a.z; u[i][3] = a.w;
-      u[i][4] = c.x; u[i][5] = c.y; u[i][6] = c.z; u[i][7] = c.w;
-    }
-    qs[r] = p.scale_log2;
-    if constexpr (!kFp16) {
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < LD; ++i)
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float2 f = unpack2<false>(u[i][w]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 126);
-      const float up = pow2i(14 - e);
-      qs[r] *= pow2i(e - 14);
-#pragma unroll
-      for (int i = 0; i < LD; ++i)
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float2 f = unpack2<false>(u[i][w]);
-          u[i][w] = pack2<true>(f.x * up, f.y * up);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < LD; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qa[i][j][r] = u[i][2 * j];
-        qa[i][j][2 + r] = u[i][2 * j + 1];
-      }
-  }
-
-  float o[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  const uint32_t ring = smem_addr(smem) + warp * R::kWarp, ring_s = ring + kStages * R::kStage;
-  const int blocks = lo < hi ? ((hi - lo + kKv8Block - 1) / kKv8Block - warp + kWarps - 1) / kWarps : 0;
-  const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
-  const int* table = p.table + static_cast<long long>(b) * p.pps;
-
-  auto page_of = [&](int i) {  // page of this warp's block i (-1: none)
-    return i < blocks ? __ldg(table + ((lo + (warp + i * kWarps) * kKv8Block) >> p.page_shift)) : -1;
-  };
-  auto fetch = [&](int i, int page) {
-    if (i < blocks) {
-      const int key0 = lo + (warp + i * kWarps) * kKv8Block;
-      bool ok = page >= 0 && page < p.num_pages;
-      if (!ok) {
-        if (lane == 0) record_status(p.status, kStatusPageTable);
-        page = 0;
-      }
-      const size_t head = static_cast<size_t>(page) * p.Hkv + hk;
-      const int in_page = key0 & ((1 << p.page_shift) - 1);
-      const size_t at = ((head << p.page_shift) + in_page) * D;
-      const size_t sc = head * ((1 << p.page_shift) / kKv8Block) + in_page / kKv8Block;
-      ok = ok && idx_ok(p.status, at, R::kBlock, pool * D) && idx_ok(p.status, sc, 1, pool / kKv8Block);
-      const int st = i % kStages;
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int c = j * 32 + lane, r = c / (D / 16), ch = c % (D / 16);
-        const bool full = ok && key0 + r < hi;
-        const uint32_t dst = ring + st * R::kStage + ring_off<D>(r, ch);
-        cp16(dst, p.k + at + c * 16, full);
-        cp16(dst + R::kBlock, p.v + at + c * 16, full);
-      }
-      if (lane < 2) cp4(ring_s + st * 16 + lane * 4, (lane ? p.vs : p.ks) + sc, ok);
-    }
-    cp_commit();
-  };
-
-  int next = page_of(0);
-  for (int i = 0; i < kStages - 1; ++i) {
-    const int page = next;
-    next = page_of(i + 1);
-    fetch(i, page);
-  }
-  for (int i = 0; i < blocks; ++i) {
-    {
-      const int page = next;
-      next = page_of(i + kStages);
-      fetch(i + kStages - 1, page);
-    }
-    cp_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t kb = ring + (i % kStages) * R::kStage, vb = kb + R::kBlock;
-    float ks, vs;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(ring_s + (i % kStages) * 16) : "memory");
-    const int key0 = lo + (warp + i * kWarps) * kKv8Block;
-
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int c = 0; c < LD; ++c) {
-        const uint4 u = lds128(kb + ring_off<D>(n * 8 + g, t + 4 * c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16(sc[n], qa[c][j], half2_of<kInt8>(w[j] & 0xFFFFu), half2_of<kInt8>(w[j] >> 16));
-      }
-
-    const bool edge = key0 + kKv8Block > min(tile_all, hi);
-    const float lv = lg2(fmaxf(vs, 1.17549435e-38f));  // a scale of zero stands for values of zero
-    uint32_t pa[4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float f = qs[r] * ks;
-      float x[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[2 * n + e] = sc[n][2 * r + e] * f;
-          if (edge && key0 + 8 * n + 2 * t + e >= min(lim[r], hi)) x[2 * n + e] = -INFINITY;
-        }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > m[r] + kLazy) {  // (false while both are -inf)
-        l[r] *= ex2(m[r] - mx);
-        m[r] = mx;
-      }
-      const float mv = mx + lv;
-      if (mv > mo[r] + kLazy) {
-        const float a = ex2(mo[r] - mv);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[j][2 * r] *= a;
-          o[j][2 * r + 1] *= a;
-        }
-        mo[r] = mv;
-      }
-      const float mm = m[r] == -INFINITY ? 0.f : m[r], mw = mo[r] == -INFINITY ? 0.f : mo[r] - lv;
-      float w[4];
-#pragma unroll
-      for (int i2 = 0; i2 < 4; ++i2) {
-        l[r] += ex2(x[i2] - mm);
-        w[i2] = ex2(x[i2] - mw);
-      }
-      pa[r] = pack2<true>(w[0], w[1]);
-      pa[2 + r] = pack2<true>(w[2], w[3]);
-    }
-
-    // O += W V: this lane's four keys (2t, 2t + 1 of both halves of the block), D / 8 columns from d = (D / 8) g
-    uint32_t v[4][D / 32];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = (k >> 1) * 8 + 2 * t + (k & 1);
-      if constexpr (D == 128) {
-        const uint4 u = lds128(vb + ring_off<D>(r, g));
-        v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
-      } else {
-        const uint2 u = lds64(vb + ring_off<D>(r, g >> 1) + (g & 1) * 8);
-        v[k][0] = u.x; v[k][1] = u.y;
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-      const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-      mma_f16(o[4 * w], pa, half2_of<kInt8>(a0 & 0xFFFFu), half2_of<kInt8>(b0 & 0xFFFFu));
-      mma_f16(o[4 * w + 1], pa, half2_of<kInt8>(a0 >> 16), half2_of<kInt8>(b0 >> 16));
-      mma_f16(o[4 * w + 2], pa, half2_of<kInt8>(a1 & 0xFFFFu), half2_of<kInt8>(b1 & 0xFFFFu));
-      mma_f16(o[4 * w + 3], pa, half2_of<kInt8>(a1 >> 16), half2_of<kInt8>(b1 >> 16));
-    }
-    __syncwarp();  // every lane has read the stage before the next fetch writes it
-  }
-  cp_wait<0>();
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sm.sums[warp] = sum;
   __syncthreads();
-
-  // merge of the four warps through shared memory: O [warp][row][d], then m, l, mo [warp][row]
-  float* ro = reinterpret_cast<float*>(smem);
-  float* rm = ro + kWarps * kRows * D;
-  float* rl = rm + kWarps * kRows;
-  float* rw = rl + kWarps * kRows;
+  r.total = sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3];
+  const int shares = shares_of(p, r.total, grid);
+  r.b = -1;
+  r.off = 0;
+  if (c >= shares) return r;  // uniform: this CTA has no share
+  const long long want = share_begin(r.total, shares, c);
+  long long before = 0;
+  for (int base = 0; base < p.B; base += kThreads) {
+    const int b = base + tid;
+    const long long n = p.B <= kThreads ? (b < p.B ? mine : 0) : (b < p.B ? item_granules<kRows>(p, b) : 0);
+    long long x = n;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    const int row = warp * kRows + g + 8 * r;
-    if (t == 0) {
-      rm[row] = m[r];
-      rl[row] = l[r];
-      rw[row] = mo[r];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    // n-tile j, column 2t + e holds d = (D / 8) (2t + e) + j
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int j = 0; j < NT; j += 4)
-        *reinterpret_cast<float4*>(ro + static_cast<size_t>(row) * D + NT * (2 * t + e) + j) =
-            make_float4(o[j][2 * r + e], o[j + 1][2 * r + e], o[j + 2][2 * r + e], o[j + 3][2 * r + e]);
-  }
-  __syncthreads();
-  for (int i = tid; i < kRows * D / 2; i += kThreads) {
-    const int row = i / (D / 2), d = i % (D / 2) * 2, rr = row0 + row;
-    if (rr >= rows) break;
-    float M = -INFINITY, W = -INFINITY;
+    __syncthreads();  // sums were read
+    if (lane == 31) sm.sums[warp] = x;
+    __syncthreads();
+    long long all = before;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      M = fmaxf(M, rm[w * kRows + row]);
-      W = fmaxf(W, rw[w * kRows + row]);
+      if (w < warp) x += sm.sums[w];
+      all += sm.sums[w];
     }
-    float sum = 0.f, a = 0.f, c = 0.f;
-    if (M > -INFINITY) {
+    x += before;  // granules up to and with this item
+    if (want < x && want >= x - n) {
+      sm.b = b;
+      sm.off = want - (x - n);
+    }
+    before = all;
+    if (want < all) break;  // uniform
+  }
+  __syncthreads();
+  r.b = sm.b;
+  r.off = sm.off;
+  return r;
+}
+
+// The unit (row tile, KV head) that granule `off` of an item with len keys lies in, its granules, and the
+// granule's number inside it.
+struct Unit {
+  int tile, hk, n, g0;
+};
+template <int kRows>
+__device__ __forceinline__ Unit unit_at(const AttParams& p, int len, long long off) {
+  Unit u;
+  for (u.tile = 0;; ++u.tile) {
+    u.n = tile_granules<kRows>(p, len, u.tile);
+    const long long here = static_cast<long long>(u.n) * p.Hkv;
+    if (off < here) break;
+    off -= here;
+  }
+  u.hk = static_cast<int>(off / u.n);
+  u.g0 = static_cast<int>(off % u.n);
+  return u;
+}
+
+// Index of a row among the rows of O [B, Nq, Hq, D], and of its LSE [B, Hq, Nq].
+__device__ __forceinline__ size_t o_row(const AttParams& p, int b, int hk, int row) {
+  return (static_cast<size_t>(b) * p.Nq + row / p.group) * p.Hq + hk * p.group + row % p.group;
+}
+__device__ __forceinline__ size_t lse_row(const AttParams& p, int b, int hk, int row) {
+  return (static_cast<size_t>(b) * p.Hq + hk * p.group + row % p.group) * p.Nq + row / p.group;
+}
+
+template <bool kFp16, bool kInt8, int D, int NG>
+__global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const AttParams p, const int o_fp32) {
+  using R = Ring<D, NG>;
+  constexpr int kRows = R::kRows, kStages = R::kStages;
+  constexpr int LD = D / 64;  // 16-byte pieces of a K row per lane
+  constexpr int MT = D / 16;  // 16-column tiles of O (M of the second product)
+  constexpr int kDShift = D == 128 ? 7 : 6;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ ScanMem scan;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int rows = p.Nq * p.group;
+  const long long outs = static_cast<long long>(p.B) * p.Nq * p.Hq;
+  const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
+
+  // rows of tiles that see no key at all, and lengths out of range (reported)
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (p.seqlens && tid == 0) {
+      const int len = __ldg(p.seqlens + b);
+      if (len < 0 || len > (p.pps << p.page_shift)) record_status(p.status, kStatusCuSeqlens);
+    }
+    const int len = keys_of(p, b);
+    for (int tile = 0; tile < p.tiles && tile_keys<kRows>(p, len, tile) == 0; ++tile) {
+      const int n = min(rows - tile * kRows, kRows) * p.Hkv;
+      for (int i = tid; i < n * (D / 2); i += kThreads) {
+        const int row = tile * kRows + i / (D / 2) / p.Hkv, hk = i / (D / 2) % p.Hkv, d = i % (D / 2) * 2;
+        const size_t at = o_row(p, b, hk, row);
+        if (!idx_ok(p.status, at, 1, outs)) continue;
+        store2<kFp16>(p.o, at * D + d, 0.f, 0.f, o_fp32 != 0);
+        if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
+      }
+    }
+  }
+
+  const Place place = find_place<kRows>(p, gridDim.x, blockIdx.x, scan);
+  if (place.b < 0) return;
+  const int shares = shares_of(p, place.total, gridDim.x);
+  long long left = share_begin(place.total, shares, blockIdx.x + 1) - share_begin(place.total, shares, blockIdx.x);
+  long long off = place.off;
+  int b = place.b;
+
+  const uint32_t ring = smem_addr(smem) + warp * R::kWarp, ring_s = ring + kStages * R::kStage;
+
+  while (left > 0) {
+    const int len = keys_of(p, b);
+    {
+      long long here = 0;
+      for (int i = 0; i < p.tiles; ++i) here += tile_granules<kRows>(p, len, i);
+      if (off >= here * p.Hkv) {  // (items without granules are passed over)
+        ++b;
+        off = 0;
+        continue;
+      }
+    }
+    const Unit u = unit_at<kRows>(p, len, off);
+    const int take = static_cast<int>(min(left, static_cast<long long>(u.n - u.g0)));
+    left -= take;
+    off += take;
+    const int row0 = u.tile * kRows, hk = u.hk;
+    const int tile_end = tile_keys<kRows>(p, len, u.tile), tile_all = row_limit(p, len, row0);
+    const int lo = u.g0 * p.granule;
+    const int hi = static_cast<int>(min(static_cast<long long>(tile_end), static_cast<long long>(lo) + static_cast<long long>(take) * p.granule));
+    const bool whole = u.g0 == 0 && take == u.n;
+
+    // the first blocks are on their way before the queries are read
+    const int blocks = ((hi - lo + kKv8Block - 1) / kKv8Block - warp + kWarps - 1) / kWarps;
+    const int* table = p.table + static_cast<long long>(b) * p.pps;
+    const int key_w = lo + warp * kKv8Block;  // first key of this warp's block 0
+    auto page_of = [&](int i) {               // page of block i (-1: none)
+      return i < blocks ? __ldg(table + ((key_w + i * (kWarps * kKv8Block)) >> p.page_shift)) : -1;
+    };
+    auto fetch = [&](int i, int st, int page) {  // block i into stage st
+      if (i < blocks) {
+        const int key0 = key_w + i * (kWarps * kKv8Block);
+        bool ok = page >= 0 && page < p.num_pages;
+        if (!ok) {
+          if (lane == 0) record_status(p.status, kStatusPageTable);
+          page = 0;
+        }
+        // first row of the block among the pool's rows
+        const long long row = ((static_cast<long long>(page) * p.Hkv + hk) << p.page_shift) + (key0 & ((1 << p.page_shift) - 1));
+        ok = ok && idx_ok(p.status, row, kKv8Block, pool);
+        const uint8_t* ksrc = p.k + (row << kDShift) + lane * 16;
+        const uint8_t* vsrc = p.v + (row << kDShift) + lane * 16;
+        const uint32_t dst = ring + st * R::kStage;
+        if (ok && key0 + kKv8Block <= hi) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const uint32_t at = dst + ring_off<D>((j * 32 + lane) / (D / 16), lane % (D / 16));
+            cp16(at, ksrc + j * 512);
+            cp16(at + R::kBlock, vsrc + j * 512);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const int r = (j * 32 + lane) / (D / 16);
+            const uint32_t at = dst + ring_off<D>(r, lane % (D / 16));
+            cp16_or_zero(at, ksrc + j * 512, ok && key0 + r < hi);
+            cp16_or_zero(at + R::kBlock, vsrc + j * 512, ok && key0 + r < hi);
+          }
+        }
+        if (lane < 2) cp4_or_zero(ring_s + st * 16 + lane * 4, (lane ? p.vs : p.ks) + (row >> 4), ok);
+      }
+      cp_commit();
+    };
+    int next = page_of(0);
+    for (int i = 0; i < kStages - 1; ++i) {
+      const int page = next;
+      next = page_of(i + 1);
+      fetch(i, i, page);
+    }
+
+    // queries: B operand, row 8 n + g, 16 values from d = 16 (t + 4 c); the scales of the rows 8 n + 2 t + e that
+    // this lane holds in the accumulators come from the lanes that read them
+    uint32_t qb[NG][LD][4][2];
+    float qs[NG][2];
+    int lim[NG][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const int row = row0 + 8 * n + g;
+      const bool in = row < rows;
+      const size_t at = o_row(p, b, hk, in ? row : row0) * D;
+      uint32_t w[LD][8];
+#pragma unroll
+      for (int c = 0; c < LD; ++c) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + 16 * (t + 4 * c));
+        const bool ok = in && idx_ok(p.status, at + 16 * (t + 4 * c), 16, outs * D);
+        const uint4 x = ok ? __ldg(src) : make_uint4(0, 0, 0, 0), y = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+        w[c][0] = x.x; w[c][1] = x.y; w[c][2] = x.z; w[c][3] = x.w;
+        w[c][4] = y.x; w[c][5] = y.y; w[c][6] = y.z; w[c][7] = y.w;
+      }
+      float down = p.scale_log2;
+      if constexpr (!kFp16) {
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < LD; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 f = unpack2<false>(w[c][j]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 126);
+        const float up = pow2i(14 - e);
+        down *= pow2i(e - 14);
+#pragma unroll
+        for (int c = 0; c < LD; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 f = unpack2<false>(w[c][j]);
+            w[c][j] = pack2<true>(f.x * up, f.y * up);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < LD; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // the four values that a word of K meets, in the order of halves_of
+          qb[n][c][j][0] = kInt8 ? __byte_perm(w[c][2 * j], w[c][2 * j + 1], 0x5410) : w[c][2 * j];
+          qb[n][c][j][1] = kInt8 ? __byte_perm(w[c][2 * j], w[c][2 * j + 1], 0x7632) : w[c][2 * j + 1];
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = row0 + 8 * n + 2 * t + e;
+        qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
+        lim[n][e] = r < rows ? min(row_limit(p, len, r), hi) : 0;
+      }
+    }
+
+    float o[NG][MT][4];
+    float m[NG][2], mo[NG][2], l[NG][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    int st = 0, st_in = kStages - 1;  // stages of block i and of block i + kStages - 1
+    for (int i = 0; i < blocks; ++i) {
+      {
+        const int page = next;
+        next = page_of(i + kStages);
+        fetch(i + kStages - 1, st_in, page);
+      }
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t kb = ring + st * R::kStage, vb = kb + R::kBlock;
+      float ks, vs;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(ring_s + st * 16) : "memory");
+      const int key0 = key_w + i * (kWarps * kKv8Block);
+
+      // S^T: element e of accumulator n: key g + 8 (e >> 1), row 8 n + 2 t + (e & 1)
+      float sc[NG][4] = {};
+#pragma unroll
+      for (int c = 0; c < LD; ++c) {
+        const uint4 x = lds128(kb + ring_off<D>(g, t + 4 * c)), y = lds128(kb + ring_off<D>(g + 8, t + 4 * c));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3;
+          halves_of<kInt8>(xw[j], a0, a2);
+          halves_of<kInt8>(yw[j], a1, a3);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) mma_f16(sc[n], a0, a1, a2, a3, qb[n][c][j][0], qb[n][c][j][1]);
+        }
+      }
+
+      const bool edge = key0 + kKv8Block > min(tile_all, hi);
+      const float lv = lg2(fmaxf(vs, 1.17549435e-38f));  // a scale of zero stands for values of zero
+      uint32_t wb[NG][2];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = sc[n][e] * (qs[n][e & 1] * ks);
+          if (edge && key0 + g + 8 * (e >> 1) >= lim[n][e & 1]) x[e] = -INFINITY;
+        }
+        // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks)
+        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        const bool past = mx[0] > m[n][0] + kLazy || mx[1] > m[n][1] + kLazy || mx[0] + lv > mo[n][0] + kLazy || mx[1] + lv > mo[n][1] + kLazy;
+        if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int s2 = 4; s2 <= 16; s2 <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], s2));
+            if (mx[e] > m[n][e]) {  // (false while both are -inf)
+              l[n][e] *= ex2(m[n][e] - mx[e]);
+              m[n][e] = mx[e];
+            }
+            const float mv = mx[e] + lv;
+            if (mv > mo[n][e]) {
+              const float f = ex2(mo[n][e] - mv);
+#pragma unroll
+              for (int i2 = 0; i2 < MT; ++i2) {
+                o[n][i2][e] *= f;
+                o[n][i2][2 + e] *= f;
+              }
+              mo[n][e] = mv;
+            }
+          }
+        }
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mm = m[n][e] == -INFINITY ? 0.f : m[n][e], mw = mo[n][e] == -INFINITY ? 0.f : mo[n][e] - lv;
+          l[n][e] += ex2(x[e] - mm) + ex2(x[2 + e] - mm);
+          w[e] = ex2(x[e] - mw);
+          w[2 + e] = ex2(x[2 + e] - mw);
+        }
+        wb[n][0] = transpose8x8(pack2<true>(w[0], w[1]));  // keys 0..7 of the block
+        wb[n][1] = transpose8x8(pack2<true>(w[2], w[3]));  // keys 8..15
+      }
+
+      // O^T += V^T W^T: this lane's keys 2t, 2t + 1 of both halves of the block, D / 8 columns from d = (D / 8) g;
+      // tile i: its rows g and g + 8 are the columns 2 i and 2 i + 1 of those
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = (k >> 1) * 8 + 2 * t + (k & 1);
+        if constexpr (D == 128) {
+          const uint4 x = lds128(vb + ring_off<D>(r, g));
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const uint2 x = lds64(vb + ring_off<D>(r, g >> 1) + (g & 1) * 8);
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        uint32_t a0, a1, a2, a3;
+        halves_of<kInt8>(pair_bytes<kInt8, 0>(v[0][w], v[1][w]), a0, a1);
+        halves_of<kInt8>(pair_bytes<kInt8, 0>(v[2][w], v[3][w]), a2, a3);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) mma_f16(o[n][2 * w], a0, a1, a2, a3, wb[n][0], wb[n][1]);
+        halves_of<kInt8>(pair_bytes<kInt8, 1>(v[0][w], v[1][w]), a0, a1);
+        halves_of<kInt8>(pair_bytes<kInt8, 1>(v[2][w], v[3][w]), a2, a3);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) mma_f16(o[n][2 * w + 1], a0, a1, a2, a3, wb[n][0], wb[n][1]);
+      }
+      st_in = st;
+      st = st + 1 == kStages ? 0 : st + 1;
+      __syncwarp();  // every lane has read the stage before the next fetch writes it
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // merge of the four warps through shared memory: O [warp][row][d], then m, l, mo [warp][row]
+    float* ro = reinterpret_cast<float*>(smem);
+    float* rm = ro + kWarps * kRows * D;
+    float* rl = rm + kWarps * kRows;
+    float* rw = rl + kWarps * kRows;
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int s2 = 4; s2 <= 16; s2 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s2);
+        const int row = warp * kRows + 8 * n + 2 * t + e;
+        if (g == 0) {
+          rm[row] = m[n][e];
+          rl[row] = sum;
+          rw[row] = mo[n][e];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; i += 2)
+          *reinterpret_cast<float4*>(ro + merge_at<D>(row, (D / 8) * g + 2 * i)) =
+              make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+      }
+    __syncthreads();
+    const int slot = 2 * blockIdx.x + (u.g0 == 0 ? 1 : 0);  // of a piece
+    for (int i = tid; i < kRows * D / 2; i += kThreads) {
+      const int row = i / (D / 2), d = i % (D / 2) * 2, rr = row0 + row;
+      if (rr >= rows) break;
+      float M = -INFINITY, W = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        sum += ex2(rm[w * kRows + row] - M) * rl[w * kRows + row];
-        const float f = ex2(rw[w * kRows + row] - W);
-        const float2 x = *reinterpret_cast<const float2*>(ro + static_cast<size_t>(w * kRows + row) * D + d);
-        a += f * x.x;
-        c += f * x.y;
+        M = fmaxf(M, rm[w * kRows + row]);
+        W = fmaxf(W, rw[w * kRows + row]);
       }
-      const float f = ex2(W - M) / sum;
-      a *= f;
-      c *= f;
+      float sum = 0.f, x0 = 0.f, x1 = 0.f;
+      if (M > -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          sum += ex2(rm[w * kRows + row] - M) * rl[w * kRows + row];
+          const float f = ex2(rw[w * kRows + row] - W);
+          const float2 x = *reinterpret_cast<const float2*>(ro + merge_at<D>(w * kRows + row, d));
+          x0 += f * x.x;
+          x1 += f * x.y;
+        }
+        const float f = ex2(W - M) / sum;
+        x0 *= f;
+        x1 *= f;
+      }
+      const float ls = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
+      if (whole) {
+        const size_t at = o_row(p, b, hk, rr);
+        if (!idx_ok(p.status, at, 1, outs)) continue;
+        store2<kFp16>(p.o, at * D + d, x0, x1, o_fp32 != 0);
+        if (d == 0) p.lse[lse_row(p, b, hk, rr)] = ls;
+      } else {
+        const size_t at = static_cast<size_t>(slot) * kRows + row;
+        if (!idx_ok(p.status, at, 1, 2LL * gridDim.x * kRows)) continue;
+        *reinterpret_cast<float2*>(p.ws_o + at * D + d) = make_float2(x0, x1);
+        if (d == 0) p.ws_l[at] = ls;
+      }
     }
-    const float ls = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
-    const int tok = rr / p.group, hq = hk * p.group + rr % p.group;
-    const size_t out = (static_cast<size_t>(b) * p.Nq + tok) * p.Hq + hq;
-    const long long outs = static_cast<long long>(p.B) * p.Nq * p.Hq;
-    if (!idx_ok(p.status, out, 1, outs)) continue;
-    if (p.S == 1) {
-      store2<kFp16>(p.o, out * D + d, a, c, o_fp32 != 0);
-      if (d == 0) p.lse[(static_cast<size_t>(b) * p.Hq + hq) * p.Nq + tok] = ls;
-    } else {
-      *reinterpret_cast<float2*>(p.ws_o + (out * p.S + split) * D + d) = make_float2(a, c);
-      if (d == 0) p.ws_l[out * p.S + split] = ls;
-    }
+    __syncthreads();  // the merge buffers are the ring of the next unit
   }
 }
 
-// One warp per output row: O = sum_s exp(lse_s - M) o_s / sum_s exp(lse_s - M), LSE = M + ln of that sum.
-template <bool kFp16, int D>
-__global__ void __launch_bounds__(128) kv8_combine_kernel(const AttParams p, const int o_fp32) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.Nq * p.Hq) return;
-  const float* wl = p.ws_l + row * p.S;
-  float M = -INFINITY;
-  for (int s = lane; s < p.S; s += 32) M = fmaxf(M, wl[s] * kLog2e);
+// Merges the pieces of the units that lie in more than one share.  CTA i looks at the border between
+// shares i and i + 1 and takes the unit it cuts, if no earlier border cuts the same one: piece 0 is the
+// end of share i, the others are the beginnings of shares i + 1, i + 2, ...  O = sum_s exp(lse_s - M) o_s /
+// sum_s exp(lse_s - M), LSE = M + ln of that sum; one warp per row.
+template <bool kFp16, int D, int NG>
+__global__ void __launch_bounds__(kThreads) kv8_combine_kernel(const AttParams p, const int o_fp32, const int grid) {
+  constexpr int kRows = 8 * NG;
+  __shared__ ScanMem scan;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x + 1;
+  const Place place = find_place<kRows>(p, grid, c, scan);
+  if (place.b < 0) return;
+  const int shares = shares_of(p, place.total, grid);
+  const Unit u = unit_at<kRows>(p, keys_of(p, place.b), place.off);
+  const long long here = share_begin(place.total, shares, c), begin = here - u.g0, end = begin + u.n;
+  if (u.g0 == 0 || begin < share_begin(place.total, shares, c - 1)) return;
+  int pieces = 1;  // beside the first
+  while (c + pieces < shares && share_begin(place.total, shares, c + pieces) < end) ++pieces;
+  auto slot = [&](int s) { return s == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + s); };
+  const int rows = min(kRows, p.Nq * p.group - u.tile * kRows);
+  for (int row = warp; row < rows; row += kWarps) {
+    auto lse_of = [&](int s) { return p.ws_l[static_cast<size_t>(slot(s)) * kRows + row] * kLog2e; };
+    float M = -INFINITY;
+    for (int s = lane; s <= pieces; s += 32) M = fmaxf(M, lse_of(s));
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[D / 32] = {}, sum = 0.f;
-  if (M > -INFINITY) {
-    for (int s = 0; s < p.S; ++s) {
-      const float w = ex2(wl[s] * kLog2e - M);
-      if (w == 0.f) continue;
-      sum += w;
-      const float2* x = reinterpret_cast<const float2*>(p.ws_o + (row * p.S + s) * D) + lane * (D / 64);
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[D / 32] = {}, sum = 0.f;
+    if (M > -INFINITY) {
+      for (int s = 0; s <= pieces; ++s) {
+        const float w = ex2(lse_of(s) - M);
+        sum += w;
+        const float2* x = reinterpret_cast<const float2*>(p.ws_o + (static_cast<size_t>(slot(s)) * kRows + row) * D) + lane * (D / 64);
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        acc[2 * e] = fmaf(w, x[e].x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(w, x[e].y, acc[2 * e + 1]);
+        for (int e = 0; e < D / 64; ++e) {
+          acc[2 * e] = fmaf(w, x[e].x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(w, x[e].y, acc[2 * e + 1]);
+        }
       }
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
     }
-    const float inv = 1.f / sum;
+    const int rr = u.tile * kRows + row;
+    const size_t at = o_row(p, place.b, u.hk, rr);
+    if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
-  }
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) store2<kFp16>(p.o, row * D + lane * (D / 32) + 2 * e, acc[2 * e], acc[2 * e + 1], o_fp32 != 0);
-  if (lane == 0) {
-    const int hq = static_cast<int>(row % p.Hq);
-    const long long tok = row / p.Hq;
-    p.lse[(tok / p.Nq * p.Hq + hq) * p.Nq + tok % p.Nq] = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
+    for (int e = 0; e < D / 64; ++e) store2<kFp16>(p.o, at * D + lane * (D / 32) + 2 * e, acc[2 * e], acc[2 * e + 1], o_fp32 != 0);
+    if (lane == 0) p.lse[lse_row(p, place.b, u.hk, rr)] = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
   }
 }
 
-// Splits of the keys: enough CTAs for four per SM, at most kMaxSplits.
-int splits_for(int B, int Nq, int Hq, int Hkv) {
-  const long long units = static_cast<long long>(B) * Hkv * ((static_cast<long long>(Nq) * (Hq / Hkv) + kRows - 1) / kRows);
-  return static_cast<int>(std::max(1LL, std::min<long long>(kMaxSplits, (148 * 4 + units - 1) / units)));
+// Rows of a tile, in groups of eight: the fewest that hold all rows, or 32.
+int groups_for(int Nq, int group) { return static_cast<int>(std::min<long long>(4, (static_cast<long long>(Nq) * group + 7) / 8)); }
+
+template <bool kFp16, bool kInt8, int D, int NG>
+int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
+  using R = Ring<D, NG>;
+  constexpr int kCtas = kPerSm<NG> * kSms;
+  auto kern = kv8_attend_kernel<kFp16, kInt8, D, NG>;
+  static PerContext<int> configured;
+  int unused = 0;
+  const int ce = configured.get(
+      &unused, [&](int*) { return static_cast<int>(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem)); });
+  if (ce != 0) return ce;
+  p.tiles = static_cast<int>((static_cast<long long>(a.Nq) * p.group + R::kRows - 1) / R::kRows);
+  p.ws_o = static_cast<float*>(a.ws);
+  p.ws_l = p.ws_o + static_cast<size_t>(2) * kCtas * R::kRows * D;
+  const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
+  p.granule = cap <= kShortKeys ? kShortKeys : kGranule;
+  // no more CTAs than the fullest tables could give work to
+  const long long most = (cap + p.granule - 1) / p.granule * p.B * p.Hkv * p.tiles;
+  const int grid = static_cast<int>(std::min<long long>(kCtas, p.granule == kGranule ? (most + kMinGranules - 1) / kMinGranules : most));
+  kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
+  if (p.granule == kGranule && grid > 1) kv8_combine_kernel<kFp16, D, NG><<<grid - 1, kThreads, 0, stream>>>(p, a.o_fp32, grid);
+  return static_cast<int>(cudaGetLastError());
 }
 
 template <bool kFp16, bool kInt8, int D>
-int launch_t(const Attend8Args& a, const AttParams& p, cudaStream_t stream) {
-  auto kern = kv8_attend_kernel<kFp16, kInt8, D>;
-  static PerContext<int> configured;
-  int unused = 0;
-  const int ce = configured.get(&unused, [&](int*) {
-    return static_cast<int>(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kSmem));
-  });
-  if (ce != 0) return ce;
-  const long long gx = static_cast<long long>(p.tiles) * p.Hkv;
-  if (gx > 0x7fffffffLL) return static_cast<int>(cudaErrorInvalidConfiguration);
-  kern<<<dim3(static_cast<unsigned>(gx), p.S, p.B), kThreads, Ring<D>::kSmem, stream>>>(p, a.o_fp32);
-  if (p.S > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.Nq * p.Hq;
-    kv8_combine_kernel<kFp16, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, a.o_fp32);
+int launch_rows(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
+  switch (groups_for(a.Nq, p.group)) {
+    case 1: return launch_t<kFp16, kInt8, D, 1>(a, p, stream);
+    case 2: return launch_t<kFp16, kInt8, D, 2>(a, p, stream);
+    case 3: return launch_t<kFp16, kInt8, D, 3>(a, p, stream);
+    default: return launch_t<kFp16, kInt8, D, 4>(a, p, stream);
   }
-  return static_cast<int>(cudaGetLastError());
 }
 
 }  // namespace
 
 size_t kv8_attend_ws_bytes(int B, int Nq, int Hq, int Hkv, int D) {
-  const int S = splits_for(B, Nq, Hq, Hkv);
-  if (S == 1) return 256;
-  const size_t n = static_cast<size_t>(S) * B * Nq * Hq;
-  return (n * (D + 1) * sizeof(float) + 255) & ~static_cast<size_t>(255);
+  const int n = groups_for(Nq, Hq / Hkv), per_sm = n == 1 ? kPerSm<1> : n == 2 ? kPerSm<2> : n == 3 ? kPerSm<3> : kPerSm<4>;
+  return static_cast<size_t>(2) * per_sm * kSms * 8 * n * (D + 1) * sizeof(float);
 }
 
 int launch_kv8_attend(const Attend8Args& a, cudaStream_t stream) {
@@ -498,22 +756,18 @@ int launch_kv8_attend(const Attend8Args& a, cudaStream_t stream) {
   p.Hq = a.Hq;
   p.Hkv = a.c.Hkv;
   p.group = a.Hq / a.c.Hkv;
-  p.tiles = static_cast<int>((static_cast<long long>(a.Nq) * p.group + kRows - 1) / kRows);
-  p.S = splits_for(p.B, p.Nq, p.Hq, p.Hkv);
   p.num_pages = a.c.num_pages;
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.c.page_size) ++p.page_shift;
   p.pps = a.c.pages_per_seq;
   p.scale_log2 = a.scale * kLog2e;
-  p.ws_o = static_cast<float*>(a.ws);
-  p.ws_l = p.ws_o + static_cast<size_t>(p.S) * p.B * p.Nq * p.Hq * a.c.D;
   p.status = a.status;
   if (a.c.D == 64) {
-    if (a.c.int8) return a.fp16 ? launch_t<true, true, 64>(a, p, stream) : launch_t<false, true, 64>(a, p, stream);
-    return a.fp16 ? launch_t<true, false, 64>(a, p, stream) : launch_t<false, false, 64>(a, p, stream);
+    if (a.c.int8) return a.fp16 ? launch_rows<true, true, 64>(a, p, stream) : launch_rows<false, true, 64>(a, p, stream);
+    return a.fp16 ? launch_rows<true, false, 64>(a, p, stream) : launch_rows<false, false, 64>(a, p, stream);
   }
-  if (a.c.int8) return a.fp16 ? launch_t<true, true, 128>(a, p, stream) : launch_t<false, true, 128>(a, p, stream);
-  return a.fp16 ? launch_t<true, false, 128>(a, p, stream) : launch_t<false, false, 128>(a, p, stream);
+  if (a.c.int8) return a.fp16 ? launch_rows<true, true, 128>(a, p, stream) : launch_rows<false, true, 128>(a, p, stream);
+  return a.fp16 ? launch_rows<true, false, 128>(a, p, stream) : launch_rows<false, false, 128>(a, p, stream);
 }
 
 }  // namespace fa

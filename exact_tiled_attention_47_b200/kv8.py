@@ -7,10 +7,13 @@ the helpers check tensors, allocate outputs and raise on errors, as those of the
 """
 from __future__ import annotations
 
+import contextlib
+import functools
 import math
 
 import exact_tiled_attention_47_b200 as fa
 
+from . import _lib
 from ._lib import load
 
 _CODES = None
@@ -58,60 +61,67 @@ def fa_kv8_attend(q, k_pages, v_pages, k_scales, v_scales, block_table, o, lse, 
                                 floats.get(o.dtype, -1) if o_dtype is None else int(o_dtype))
 
 
-class on_stream:
-    """The device of the tensors and the caller's stream (a torch stream, a handle, or None for the
-    current one) made current, so that what a helper allocates belongs to the stream its kernels run on."""
+def enter(device, stream):
+    """(context, raw stream) of a helper's call on tensors of this device: the context makes their device and
+    the caller's stream current, so that what the helper allocates belongs to the stream its kernels run on;
+    it is None where both already are."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None and device.index == torch.cuda.current_device():
+        return None, torch._C._cuda_getCurrentRawStream(device.index)
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack, torch.cuda.current_stream(device).cuda_stream
 
-    __slots__ = ("stack",)
 
-    def __init__(self, device, stream):
-        import torch
-        self.stack = []
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        if device.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-            if stream.device != device:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self.stack.append(torch.cuda.stream(stream))
+def in_context(context, f, *args):
+    """f(*args) inside a context of enter()."""
+    if context is None:
+        return f(*args)
+    with context:
+        return f(*args)
 
-    def __enter__(self):
-        for c in self.stack:
-            c.__enter__()
 
-    def __exit__(self, *exc):
-        for c in reversed(self.stack):
-            c.__exit__(*exc)
+def alike(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
 
 
 def check_tensor(name, t, dtype, shape, device):
     """Raises ValueError unless t is a contiguous tensor of this dtype, shape and device."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if not alike(t, dtype, shape, device):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {device}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device} with strides {list(t.stride())}")
 
 
 def _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, device):
+    """(num_pages, Hkv, page_size, pages_per_seq, code type) of a cache; ValueError unless its tensors fit together."""
     import torch
-    if k_pages.dim() != 4 or k_pages.dtype not in _types()[0]:
+    code = _types()[0].get(k_pages.dtype)
+    shape = k_pages.shape
+    if code is None or len(shape) != 4:
         raise ValueError("k_pages: expected [num_pages, Hkv, page_size, D] of torch.float8_e4m3fn or torch.int8")
-    num_pages, heads, page_size, dim = k_pages.shape
-    if Hkv is not None and heads != Hkv or dim != D:
-        raise ValueError(f"k_pages {list(k_pages.shape)} does not hold the given heads or head dimension")
-    check_tensor("k_pages", k_pages, k_pages.dtype, (num_pages, heads, page_size, dim), device)
-    check_tensor("v_pages", v_pages, k_pages.dtype, (num_pages, heads, page_size, dim), device)
+    num_pages, heads, page_size, dim = shape
+    if (Hkv is not None and heads != Hkv) or dim != D:
+        raise ValueError(f"k_pages {list(shape)} does not hold the given heads or head dimension")
     scales = (num_pages, heads, page_size // 16)
+    check_tensor("k_pages", k_pages, k_pages.dtype, shape, device)
+    check_tensor("v_pages", v_pages, k_pages.dtype, shape, device)
     check_tensor("k_scales", k_scales, torch.float32, scales, device)
     check_tensor("v_scales", v_scales, torch.float32, scales, device)
     if block_table.dim() != 2:
         raise ValueError("block_table: expected [B, pages_per_seq]")
-    check_tensor("block_table", block_table, torch.int32, (B, block_table.shape[1]), device)
+    pages_per_seq = block_table.shape[1]
+    check_tensor("block_table", block_table, torch.int32, (B, pages_per_seq), device)
     if seqlens_k is not None:
         check_tensor("seqlens_k", seqlens_k, torch.int32, (B,), device)
-    return num_pages, heads, page_size
+    return num_pages, heads, page_size, pages_per_seq, code
 
 
 def new_kv8_cache(num_pages, page_size, Hkv, D, dtype=None, device="cuda"):
@@ -135,17 +145,28 @@ def append_kv8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_
     import torch
     B, Nt, Hkv, D = k.shape
     dev = k.device
-    num_pages, _, page_size = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, dev)
+    num_pages, _, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, dev)
     if new_lens is not None:
         check_tensor("new_lens", new_lens, torch.int32, (B,), dev)
     if v.dtype is not k.dtype or v.shape != k.shape or v.device != dev:
         raise ValueError("k and v must be alike")
-    with on_stream(dev, stream):
-        k, v = k.contiguous(), v.contiguous()
-        st = fa_kv8_append(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, new_lens, B, Nt, Hkv, num_pages, page_size,
-                           block_table.shape[1], D)
+    context, raw = enter(dev, stream)
+
+    def call():
+        rk, rv = (k, v) if k.is_contiguous() and v.is_contiguous() else (k.contiguous(), v.contiguous())
+        return (_lib._lib or load()).fa_kv8_append(
+            rk.data_ptr(), rv.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_table.data_ptr(), seqlens_k.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, Nt, Hkv, num_pages,
+            page_size, pps, D, raw, _types()[1].get(k.dtype, -1), code)
+
+    st = in_context(context, call)
     if st != fa.FA_OK:
         raise fa.FAError(st, "fa_kv8_append")
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(*sizes):
+    return max(1, fa_kv8_attend_workspace_bytes(*sizes))
 
 
 def attend_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k=None, scale=None, out_dtype=None, workspace=None,
@@ -158,19 +179,25 @@ def attend_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k=N
     import torch
     B, Nq, Hq, D = q.shape
     dev = q.device
-    num_pages, Hkv, page_size = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, None, D, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with on_stream(dev, stream):
-        q = q.contiguous()
-        if workspace is None:
-            workspace = torch.empty(max(1, fa_kv8_attend_workspace_bytes(B, Nq, Hq, Hkv, D)), device=dev, dtype=torch.uint8)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous tensor on the device of q")
-        o = torch.empty((B, Nq, Hq, D), device=dev, dtype=q.dtype if out_dtype is None else out_dtype)
+    num_pages, Hkv, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, None, D, dev)
+    floats = _types()[1]
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace: expected a contiguous tensor on the device of q")
+    context, raw = enter(dev, stream)
+
+    def call():
+        rq = q if q.is_contiguous() else q.contiguous()
+        ws = torch.empty(_workspace_bytes(B, Nq, Hq, Hkv, D), device=dev, dtype=torch.uint8) if workspace is None else workspace
+        o = torch.empty_like(rq, dtype=out_dtype)
         lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
-        st = fa_kv8_attend(q, k_pages, v_pages, k_scales, v_scales, block_table, o, lse, B, Nq, Hq, Hkv, num_pages, page_size,
-                           block_table.shape[1], D, scale, seqlens_k, workspace)
+        st = (_lib._lib or load()).fa_kv8_attend(
+            rq.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(),
+            o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, num_pages, page_size, pps, D, 1.0 / math.sqrt(D) if scale is None else scale,
+            None if seqlens_k is None else seqlens_k.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), raw,
+            floats.get(q.dtype, -1), code, floats.get(o.dtype, -1))
+        return st, o, lse
+
+    st, o, lse = in_context(context, call)
     if st != fa.FA_OK:
         raise fa.FAError(st, "fa_kv8_attend")
     return o, lse

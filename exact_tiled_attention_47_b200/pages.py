@@ -9,15 +9,17 @@ device finds (a slot named twice, no free pages) are read with ``fa_device_statu
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import exact_tiled_attention_47_b200 as fa
 
+from . import _lib
 from ._lib import load
-from .kv8 import check_tensor, on_stream
+from .kv8 import check_tensor, enter, in_context
 
 
 def _pointers(pools):
-    return (ctypes.c_void_p * len(pools))(*[fa._ptr(t) for t in pools])
+    return (ctypes.c_void_p * len(pools))(*[t if isinstance(t, int) else t.data_ptr() for t in pools])
 
 
 def _sizes(page_bytes):
@@ -84,12 +86,13 @@ def _check_state(block_table, seqlens, refcount):
     import torch
     if block_table.dim() != 2 or refcount.dim() != 1:
         raise ValueError("expected block_table [S, pages_per_seq] and refcount [num_pages]")
-    S, pages_per_seq = block_table.shape
+    S, pages_per_seq = shape = block_table.shape
     dev = block_table.device
-    check_tensor("block_table", block_table, torch.int32, (S, pages_per_seq), dev)
+    num_pages = refcount.shape[0]
+    check_tensor("block_table", block_table, torch.int32, shape, dev)
     check_tensor("seqlens", seqlens, torch.int32, (S,), dev)
-    check_tensor("refcount", refcount, torch.int32, (refcount.numel(),), dev)
-    return S, pages_per_seq, refcount.numel(), dev
+    check_tensor("refcount", refcount, torch.int32, (num_pages,), dev)
+    return S, pages_per_seq, num_pages, dev
 
 
 def _check_list(name, t, n, dev):
@@ -104,17 +107,27 @@ def _page_bytes(pools, num_pages, dev):
     for t in pools:
         if t.dim() < 1 or t.shape[0] != num_pages or t.device != dev or not t.is_contiguous():
             raise ValueError(f"pools: expected contiguous tensors of {num_pages} pages on {dev}, got {list(t.shape)} on {t.device}")
-        out.append(t.numel() // num_pages * t.element_size())
+        out.append(t.nbytes // num_pages)
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(*sizes):
+    return max(1, fa_pages_workspace_bytes(*sizes))
+
+
+def _check_workspace(workspace, dev):
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace: expected a contiguous tensor on the device of the state")
+
+
 def _workspace(workspace, n, S, num_pages, dev):
+    """(tensor, bytes), allocated on the current stream where the caller gave none."""
     import torch
     if workspace is None:
-        return torch.empty(max(1, fa_pages_workspace_bytes(n, S, num_pages)), device=dev, dtype=torch.uint8)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous tensor on the device of the state")
-    return workspace
+        need = _workspace_bytes(n, S, num_pages)
+        return torch.empty(need, device=dev, dtype=torch.uint8), need
+    return workspace, workspace.nbytes
 
 
 def _raise(st, where):
@@ -128,12 +141,18 @@ def extend_pages(block_table, seqlens, refcount, page_size, add, slots=None, wor
     n = _check_list("add", add, None, dev)
     if slots is not None:
         _check_list("slots", slots, n, dev)
+    _check_workspace(workspace, dev)
+    context, raw = enter(dev, stream)
     if n == 0:
         return
-    with on_stream(dev, stream):
-        ws = _workspace(workspace, n, S, num_pages, dev)
-        st = fa_pages_extend(block_table, seqlens, refcount, slots, add, n, S, pps, num_pages, page_size, ws)
-    _raise(st, "fa_pages_extend")
+
+    def call():
+        ws, size = _workspace(workspace, n, S, num_pages, dev)
+        return (_lib._lib or load()).fa_pages_extend(
+            block_table.data_ptr(), seqlens.data_ptr(), refcount.data_ptr(), None if slots is None else slots.data_ptr(), add.data_ptr(), n,
+            S, pps, num_pages, page_size, ws.data_ptr(), size, raw)
+
+    _raise(in_context(context, call), "fa_pages_extend")
 
 
 def fork_pages(block_table, seqlens, refcount, page_size, src, dst, pools, workspace=None, stream=None):
@@ -142,23 +161,33 @@ def fork_pages(block_table, seqlens, refcount, page_size, src, dst, pools, works
     n = _check_list("src", src, None, dev)
     _check_list("dst", dst, n, dev)
     sizes = _page_bytes(pools, num_pages, dev)
+    _check_workspace(workspace, dev)
+    context, raw = enter(dev, stream)
     if n == 0:
         return
-    with on_stream(dev, stream):
-        ws = _workspace(workspace, n, S, num_pages, dev)
-        st = fa_pages_fork(block_table, seqlens, refcount, src, dst, n, S, pps, num_pages, page_size, pools, sizes, ws)
-    _raise(st, "fa_pages_fork")
+
+    def call():
+        ws, size = _workspace(workspace, n, S, num_pages, dev)
+        return (_lib._lib or load()).fa_pages_fork(
+            block_table.data_ptr(), seqlens.data_ptr(), refcount.data_ptr(), src.data_ptr(), dst.data_ptr(), n, S, pps, num_pages, page_size,
+            _pointers(pools), _sizes(sizes), len(sizes), ws.data_ptr(), size, raw)
+
+    _raise(in_context(context, call), "fa_pages_fork")
 
 
 def free_pages(block_table, seqlens, refcount, page_size, slots, stream=None):
     """Empty slots (int32 [n]) and give back the pages that nobody else holds."""
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     n = _check_list("slots", slots, None, dev)
+    context, raw = enter(dev, stream)
     if n == 0:
         return
-    with on_stream(dev, stream):
-        st = fa_pages_free(block_table, seqlens, refcount, slots, n, S, pps, num_pages, page_size)
-    _raise(st, "fa_pages_free")
+
+    def call():
+        return (_lib._lib or load()).fa_pages_free(block_table.data_ptr(), seqlens.data_ptr(), refcount.data_ptr(), slots.data_ptr(), n, S, pps,
+                                                   num_pages, page_size, raw)
+
+    _raise(in_context(context, call), "fa_pages_free")
 
 
 def compact_pages(block_table, seqlens, refcount, page_size, pools, in_place=False, workspace=None, stream=None):
@@ -170,13 +199,21 @@ def compact_pages(block_table, seqlens, refcount, page_size, pools, in_place=Fal
     import torch
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     sizes = _page_bytes(pools, num_pages, dev)
-    with on_stream(dev, stream):
+    _check_workspace(workspace, dev)
+    context, raw = enter(dev, stream)
+
+    def call():
         table_out, ref_out = (block_table, refcount) if in_place else (torch.empty_like(block_table), torch.empty_like(refcount))
         remap, n_live = torch.empty_like(refcount), torch.empty(1, device=dev, dtype=torch.int32)
-        ws = _workspace(workspace, 1, S, num_pages, dev)
-        st = fa_pages_compact(block_table, seqlens, refcount, table_out, ref_out, remap, n_live, S, pps, num_pages, page_size, pools, sizes, ws)
+        ws, size = _workspace(workspace, 1, S, num_pages, dev)
+        st = (_lib._lib or load()).fa_pages_compact(
+            block_table.data_ptr(), seqlens.data_ptr(), refcount.data_ptr(), table_out.data_ptr(), ref_out.data_ptr(), remap.data_ptr(),
+            n_live.data_ptr(), S, pps, num_pages, page_size, _pointers(pools), _sizes(sizes), len(sizes), ws.data_ptr(), size, raw)
+        return st, (table_out, ref_out, remap, n_live)
+
+    st, out = in_context(context, call)
     _raise(st, "fa_pages_compact")
-    return table_out, ref_out, remap, n_live
+    return out
 
 
 def copy_pages(src_pools, dst_pools, src, dst, workspace=None, stream=None):
@@ -190,9 +227,14 @@ def copy_pages(src_pools, dst_pools, src, dst, workspace=None, stream=None):
     sizes = _page_bytes(src_pools, a, dev)
     if sizes != _page_bytes(dst_pools, b, dev):
         raise ValueError("source and destination pools have pages of unlike sizes")
+    _check_workspace(workspace, dev)
+    context, raw = enter(dev, stream)
     if n == 0:
         return
-    with on_stream(dev, stream):
-        ws = _workspace(workspace, n, 1, max(a, b), dev)
-        st = fa_pages_copy(src_pools, dst_pools, sizes, src, dst, n, a, b, ws)
-    _raise(st, "fa_pages_copy")
+
+    def call():
+        ws, size = _workspace(workspace, n, 1, max(a, b), dev)
+        return (_lib._lib or load()).fa_pages_copy(_pointers(src_pools), _pointers(dst_pools), _sizes(sizes), len(sizes), src.data_ptr(),
+                                                   dst.data_ptr(), n, a, b, ws.data_ptr(), size, raw)
+
+    _raise(in_context(context, call), "fa_pages_copy")
