@@ -42,6 +42,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLazy = 8.f;  // log2 units by which a maximum may be exceeded before it is raised
+constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that differences with -inf are defined)
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
 constexpr int kSms = 148;
 constexpr int kGranule = 64;      // keys: one block of 16 for each warp
@@ -212,7 +213,13 @@ __device__ __forceinline__ int shares_of(const AttParams& p, long long total, in
   const int least = p.granule == kGranule ? kMinGranules : 1;
   return static_cast<int>(min(static_cast<long long>(grid), (total + least - 1) / least));
 }
-__device__ __forceinline__ long long share_begin(long long total, int shares, int c) { return total * c / shares; }
+__device__ __forceinline__ long long share_begin(long long total, int shares, int c) {
+  if (total < (1LL << 31)) {  // (a 64-bit division takes a hundred instructions)
+    const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(shares), r = static_cast<unsigned>(total) % static_cast<unsigned>(shares);
+    return static_cast<long long>(q) * c + min(c, static_cast<int>(r));
+  }
+  return total / shares * c + min(static_cast<long long>(c), total % shares);
+}
 
 // The place of the first granule of share c: a scan of the items' granules, a CTA's worth at a time, once
 // for the total and (with more items than threads) once to find the place.  Collective.
@@ -279,8 +286,13 @@ __device__ __forceinline__ Unit unit_at(const AttParams& p, int len, long long o
     if (off < here) break;
     off -= here;
   }
-  u.hk = static_cast<int>(off / u.n);
-  u.g0 = static_cast<int>(off % u.n);
+  if (off < (1LL << 31)) {
+    u.hk = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(u.n));
+    u.g0 = static_cast<int>(static_cast<unsigned>(off) % static_cast<unsigned>(u.n));
+  } else {
+    u.hk = static_cast<int>(off / u.n);
+    u.g0 = static_cast<int>(off % u.n);
+  }
   return u;
 }
 
@@ -326,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
     }
   }
 
+  asm volatile("griddepcontrol.launch_dependents;");
   const Place place = find_place<kRows>(p, gridDim.x, blockIdx.x, scan);
   if (place.b < 0) return;
   const int shares = shares_of(p, place.total, gridDim.x);
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
     }
 
@@ -506,46 +519,57 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       uint32_t wb[NG][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        float x[4];
+        const float f[2] = {qs[n][0] * ks, qs[n][1] * ks};
+        if (edge) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = sc[n][e] * (qs[n][e & 1] * ks);
-          if (edge && key0 + g + 8 * (e >> 1) >= lim[n][e & 1]) x[e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (key0 + g + 8 * (e >> 1) >= lim[n][e & 1]) sc[n][e] = -INFINITY;
         }
         // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks)
-        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-        const bool past = mx[0] > m[n][0] + kLazy || mx[1] > m[n][1] + kLazy || mx[0] + lv > mo[n][0] + kLazy || mx[1] + lv > mo[n][1] + kLazy;
+        float mx[2];
+        bool past = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float top = fmaxf(sc[n][e], sc[n][2 + e]);
+          mx[e] = top == -INFINITY ? -INFINITY : top * f[e];  // (-inf stays what it is where the scale is zero)
+          past |= mx[e] > fminf(m[n][e], mo[n][e] - lv) + kLazy;
+        }
         if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int s2 = 4; s2 <= 16; s2 <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], s2));
-            if (mx[e] > m[n][e]) {  // (false while both are -inf)
+            if (mx[e] > m[n][e]) {
               l[n][e] *= ex2(m[n][e] - mx[e]);
               m[n][e] = mx[e];
             }
             const float mv = mx[e] + lv;
             if (mv > mo[n][e]) {
-              const float f = ex2(mo[n][e] - mv);
+              const float a = ex2(mo[n][e] - mv);
 #pragma unroll
               for (int i2 = 0; i2 < MT; ++i2) {
-                o[n][i2][e] *= f;
-                o[n][i2][2 + e] *= f;
+                o[n][i2][e] *= a;
+                o[n][i2][2 + e] *= a;
               }
               mo[n][e] = mv;
             }
           }
         }
-        float w[4];
+        float p2[4], w[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mm = m[n][e] == -INFINITY ? 0.f : m[n][e], mw = mo[n][e] == -INFINITY ? 0.f : mo[n][e] - lv;
-          l[n][e] += ex2(x[e] - mm) + ex2(x[2 + e] - mm);
-          w[e] = ex2(x[e] - mw);
-          w[2 + e] = ex2(x[2 + e] - mw);
+        for (int e = 0; e < 4; ++e) {
+          p2[e] = fmaf(sc[n][e], f[e & 1], -m[n][e & 1]);
+          w[e] = fmaf(sc[n][e], f[e & 1], lv - mo[n][e & 1]);
         }
-        wb[n][0] = transpose8x8(pack2<true>(w[0], w[1]));  // keys 0..7 of the block
-        wb[n][1] = transpose8x8(pack2<true>(w[2], w[3]));  // keys 8..15
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (sc[n][e] == -INFINITY) p2[e] = w[e] = -INFINITY;
+        }
+        l[n][0] += ex2(p2[0]) + ex2(p2[2]);
+        l[n][1] += ex2(p2[1]) + ex2(p2[3]);
+        wb[n][0] = transpose8x8(pack2<true>(ex2(w[0]), ex2(w[1])));  // keys 0..7 of the block
+        wb[n][1] = transpose8x8(pack2<true>(ex2(w[2]), ex2(w[3])));  // keys 8..15
       }
 
       // O^T += V^T W^T: this lane's keys 2t, 2t + 1 of both halves of the block, D / 8 columns from d = (D / 8) g;
@@ -581,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
     cp_wait<0>();
     __syncthreads();
 
-    // merge of the four warps through shared memory: O [warp][row][d], then m, l, mo [warp][row]
+    // merge of the four warps through shared memory: O [warp][row][d], then m, l, mo [warp][row]; a row's
+    // factors (one per warp) and its place take the room of the latter
     float* ro = reinterpret_cast<float*>(smem);
     float* rm = ro + kWarps * kRows * D;
     float* rl = rm + kWarps * kRows;
@@ -606,40 +631,50 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       }
     __syncthreads();
     const int slot = 2 * blockIdx.x + (u.g0 == 0 ? 1 : 0);  // of a piece
-    for (int i = tid; i < kRows * D / 2; i += kThreads) {
-      const int row = i / (D / 2), d = i % (D / 2) * 2, rr = row0 + row;
-      if (rr >= rows) break;
-      float M = -INFINITY, W = -INFINITY;
+    if (tid < kRows && row0 + tid < rows) {
+      const int rr = row0 + tid;
+      float M = kNone, W = kNone, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, rm[w * kRows + row]);
-        W = fmaxf(W, rw[w * kRows + row]);
+        M = fmaxf(M, rm[w * kRows + tid]);
+        W = fmaxf(W, rw[w * kRows + tid]);
       }
-      float sum = 0.f, x0 = 0.f, x1 = 0.f;
-      if (M > -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          sum += ex2(rm[w * kRows + row] - M) * rl[w * kRows + row];
-          const float f = ex2(rw[w * kRows + row] - W);
-          const float2 x = *reinterpret_cast<const float2*>(ro + merge_at<D>(w * kRows + row, d));
-          x0 += f * x.x;
-          x1 += f * x.y;
-        }
-        const float f = ex2(W - M) / sum;
-        x0 *= f;
-        x1 *= f;
-      }
-      const float ls = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
+      for (int w = 0; w < kWarps; ++w) sum += ex2(rm[w * kRows + tid] - M) * rl[w * kRows + tid];
+      const bool none = M == kNone;
+      const float f = none ? 0.f : ex2(W - M) / sum;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) rw[w * kRows + tid] = ex2(rw[w * kRows + tid] - W) * f;
+      const float ls = none ? -INFINITY : (M + lg2(sum)) * kLn2;
       if (whole) {
-        const size_t at = o_row(p, b, hk, rr);
+        const size_t at = lse_row(p, b, hk, rr);
+        if (idx_ok(p.status, at, 1, outs)) p.lse[at] = ls;
+        reinterpret_cast<int*>(rl)[tid] = static_cast<int>(o_row(p, b, hk, rr));  // (below 2^31)
+      } else if (idx_ok(p.status, static_cast<long long>(slot) * kRows + tid, 1, 2LL * gridDim.x * kRows)) {
+        p.ws_l[static_cast<size_t>(slot) * kRows + tid] = ls;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < min(kRows, rows - row0) * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = rw[w * kRows + row];
+        const float4 y = *reinterpret_cast<const float4*>(ro + merge_at<D>(w * kRows + row, d));
+        x.x = fmaf(f, y.x, x.x);
+        x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z);
+        x.w = fmaf(f, y.w, x.w);
+      }
+      if (whole) {
+        const size_t at = static_cast<size_t>(reinterpret_cast<const int*>(rl)[row]);
         if (!idx_ok(p.status, at, 1, outs)) continue;
-        store2<kFp16>(p.o, at * D + d, x0, x1, o_fp32 != 0);
-        if (d == 0) p.lse[lse_row(p, b, hk, rr)] = ls;
+        store2<kFp16>(p.o, at * D + d, x.x, x.y, o_fp32 != 0);
+        store2<kFp16>(p.o, at * D + d + 2, x.z, x.w, o_fp32 != 0);
       } else {
         const size_t at = static_cast<size_t>(slot) * kRows + row;
-        if (!idx_ok(p.status, at, 1, 2LL * gridDim.x * kRows)) continue;
-        *reinterpret_cast<float2*>(p.ws_o + at * D + d) = make_float2(x0, x1);
-        if (d == 0) p.ws_l[at] = ls;
+        if (idx_ok(p.status, at, 1, 2LL * gridDim.x * kRows)) *reinterpret_cast<float4*>(p.ws_o + at * D + d) = x;
       }
     }
     __syncthreads();  // the merge buffers are the ring of the next unit
@@ -652,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
 // sum_s exp(lse_s - M), LSE = M + ln of that sum; one warp per row.
 template <bool kFp16, int D, int NG>
 __global__ void __launch_bounds__(kThreads) kv8_combine_kernel(const AttParams p, const int o_fp32, const int grid) {
-  constexpr int kRows = 8 * NG;
+  constexpr int kRows = 8 * NG, PER = D / 32, RPW = 2 * NG;  // rows of a warp, all under way at once
   __shared__ ScanMem scan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x + 1;
@@ -664,41 +699,59 @@ __global__ void __launch_bounds__(kThreads) kv8_combine_kernel(const AttParams p
   if (u.g0 == 0 || begin < share_begin(place.total, shares, c - 1)) return;
   int pieces = 1;  // beside the first
   while (c + pieces < shares && share_begin(place.total, shares, c + pieces) < end) ++pieces;
-  auto slot = [&](int s) { return s == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + s); };
+  auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + s)) * kRows; };
   const int rows = min(kRows, p.Nq * p.group - u.tile * kRows);
-  for (int row = warp; row < rows; row += kWarps) {
-    auto lse_of = [&](int s) { return p.ws_l[static_cast<size_t>(slot(s)) * kRows + row] * kLog2e; };
-    float M = -INFINITY;
-    for (int s = lane; s <= pieces; s += 32) M = fmaxf(M, lse_of(s));
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+
+  float M[RPW], sum[RPW], acc[RPW][PER];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[D / 32] = {}, sum = 0.f;
-    if (M > -INFINITY) {
-      for (int s = 0; s <= pieces; ++s) {
-        const float w = ex2(lse_of(s) - M);
-        sum += w;
-        const float2* x = reinterpret_cast<const float2*>(p.ws_o + (static_cast<size_t>(slot(s)) * kRows + row) * D) + lane * (D / 64);
+  for (int i = 0; i < RPW; ++i) {
+    M[i] = kNone;
+    sum[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          acc[2 * e] = fmaf(w, x[e].x, acc[2 * e]);
-          acc[2 * e + 1] = fmaf(w, x[e].y, acc[2 * e + 1]);
-        }
-      }
-      const float inv = 1.f / sum;
+    for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
+  }
+  for (int s = 0; s <= pieces; ++s)
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] *= inv;
+    for (int i = 0; i < RPW; ++i) {
+      const int row = warp + i * kWarps;
+      if (row < rows) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
     }
-    const int rr = u.tile * kRows + row;
+  for (int s = 0; s <= pieces; ++s)
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const int row = warp + i * kWarps;
+      if (row >= rows) continue;
+      const float w = ex2(p.ws_l[slot(s) + row] * kLog2e - M[i]);
+      sum[i] += w;
+      const float2* x = reinterpret_cast<const float2*>(p.ws_o + (slot(s) + row) * D) + lane * (PER / 2);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) {
+        const float2 y = x[e];
+        acc[i][2 * e] = fmaf(w, y.x, acc[i][2 * e]);
+        acc[i][2 * e + 1] = fmaf(w, y.y, acc[i][2 * e + 1]);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < RPW; ++i) {
+    const int row = warp + i * kWarps, rr = u.tile * kRows + row;
+    if (row >= rows) continue;
+    const bool none = M[i] == kNone;
+    const float inv = none ? 0.f : 1.f / sum[i];
     const size_t at = o_row(p, place.b, u.hk, rr);
     if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) store2<kFp16>(p.o, at * D + lane * (D / 32) + 2 * e, acc[2 * e], acc[2 * e + 1], o_fp32 != 0);
-    if (lane == 0) p.lse[lse_row(p, place.b, u.hk, rr)] = M > -INFINITY ? (M + lg2(sum)) * kLn2 : -INFINITY;
+    for (int e = 0; e < PER / 2; ++e)
+      store2<kFp16>(p.o, at * D + lane * PER + 2 * e, acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv, o_fp32 != 0);
+    if (lane == 0) p.lse[lse_row(p, place.b, u.hk, rr)] = none ? -INFINITY : (M[i] + lg2(sum[i])) * kLn2;
   }
 }
 
-// Rows of a tile, in groups of eight: the fewest that hold all rows, or 32.
-int groups_for(int Nq, int group) { return static_cast<int>(std::min<long long>(4, (static_cast<long long>(Nq) * group + 7) / 8)); }
+// Rows of a tile, in groups of eight: as many tiles as 32 rows each take, of even size.
+int groups_for(int Nq, int group) {
+  const long long all = (static_cast<long long>(Nq) * group + 7) / 8, tiles = (all + 3) / 4;
+  return static_cast<int>((all + tiles - 1) / tiles);
+}
 
 template <bool kFp16, bool kInt8, int D, int NG>
 int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
@@ -719,7 +772,20 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   const long long most = (cap + p.granule - 1) / p.granule * p.B * p.Hkv * p.tiles;
   const int grid = static_cast<int>(std::min<long long>(kCtas, p.granule == kGranule ? (most + kMinGranules - 1) / kMinGranules : most));
   kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
-  if (p.granule == kGranule && grid > 1) kv8_combine_kernel<kFp16, D, NG><<<grid - 1, kThreads, 0, stream>>>(p, a.o_fp32, grid);
+  if (p.granule == kGranule && grid > 1) {
+    // launched while the first kernel still runs: it finds its place meanwhile and waits for the pieces
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid - 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kFp16, D, NG>, static_cast<const AttParams&>(p), static_cast<int>(a.o_fp32), grid);
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
   return static_cast<int>(cudaGetLastError());
 }
 
