@@ -18,8 +18,8 @@
 //   S^T [16 keys x 8 rows]   = K [16 keys x D] Q^T,   O^T [D x 8 rows] += V^T [D x 16 keys] W^T [16 keys x 8 rows];
 // the weights go from the accumulator's layout to the operand's with a movmatrix.
 // Work is cut evenly over the CTAs (two to four per SM), whatever the lengths are: the
-// granules (64 keys) of all units (sequence, row tile, KV head) are numbered through, CTA c takes the
-// c-th equal share, which may begin and end inside a unit, and finds its place with a scan over the
+// granules (64 keys) of all units (sequence, row tile, KV head) are numbered through, with a few more for
+// each unit's fixed cost, and CTA c takes the c-th equal share, which may begin and end inside a unit, and finds its place with a scan over the
 // lengths.  A unit that lies in one share is written at once; the pieces of the others go to the
 // workspace (at most two per CTA) and are merged in order by a second kernel.  Warp w of the four takes every
 // fourth block of 16 keys: a block has one scale per pool and lies in one page, so a warp needs nothing
@@ -46,7 +46,8 @@ constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that diff
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
 constexpr int kSms = 148;
 constexpr int kGranule = 64;      // keys: one block of 16 for each warp
-constexpr int kMinGranules = 4;   // of a share: shorter ones cost more to merge than to read
+constexpr int kMinShare = 8;      // granules (a unit's fixed cost included) of a share: shorter ones cost more to merge than to read
+constexpr int kUnitCost = 4;      // granules that the fixed cost of a unit (queries, filling the ring, merging the warps) stands for
 constexpr int kShortKeys = 512;   // tables up to this many keys: a granule is a whole unit, and nothing is merged
 
 struct AttParams {
@@ -63,14 +64,16 @@ struct AttParams {
   float* ws_l;  // [2 * shares, rows of a tile]
   int B, Nq, Hq, Hkv, group, tiles;
   int granule;  // keys
+  int over;     // kUnitCost, or 0 where a granule is a whole unit
   int num_pages, page_shift, pps;
   float scale_log2;
   int* status;
 };
 
-// CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.
+// CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.  Four of
+// one group leave 128 registers and less overlap inside a warp: 200 us where three take 193 (4 x 131072).
 template <int NG>
-constexpr int kPerSm = NG == 1 ? 4 : NG == 2 ? 3 : 2;
+constexpr int kPerSm = NG <= 2 ? 3 : 2;
 
 template <int D, int NG>
 struct Ring {
@@ -187,17 +190,20 @@ template <int kRows>
 __device__ __forceinline__ int tile_granules(const AttParams& p, int len, int tile) {
   return (tile_keys<kRows>(p, len, tile) + p.granule - 1) / p.granule;
 }
+// Cost of an item: the granules of its units and the units' fixed costs (a unit without granules has none).
 template <int kRows>
-__device__ __forceinline__ long long item_granules(const AttParams& p, int b) {
-  const int len = keys_of(p, b);
+__device__ __forceinline__ long long item_cost(const AttParams& p, int len) {
   long long n = 0;
-  for (int i = 0; i < p.tiles; ++i) n += tile_granules<kRows>(p, len, i);
+  for (int i = 0; i < p.tiles; ++i) {
+    const int m = tile_granules<kRows>(p, len, i);
+    n += m > 0 ? m + p.over : 0;
+  }
   return n * p.Hkv;
 }
 
-// Where a share begins: item b, granule `off` among the item's.
+// Where a share begins: item b, `off` of the item's cost.
 struct Place {
-  long long total;  // granules of all items
+  long long total;  // cost of all items
   long long off;
   int b;
 };
@@ -208,9 +214,9 @@ struct ScanMem {
   int b;
 };
 
-// Number of shares of `total` granules, and the first granule of share c.
+// Number of shares of a total cost, and where share c begins.
 __device__ __forceinline__ int shares_of(const AttParams& p, long long total, int grid) {
-  const int least = p.granule == kGranule ? kMinGranules : 1;
+  const int least = p.over ? kMinShare : 1;
   return static_cast<int>(min(static_cast<long long>(grid), (total + least - 1) / least));
 }
 __device__ __forceinline__ long long share_begin(long long total, int shares, int c) {
@@ -221,14 +227,14 @@ __device__ __forceinline__ long long share_begin(long long total, int shares, in
   return total / shares * c + min(static_cast<long long>(c), total % shares);
 }
 
-// The place of the first granule of share c: a scan of the items' granules, a CTA's worth at a time, once
+// The place where share c begins: a scan of the items' costs, a CTA's worth at a time, once
 // for the total and (with more items than threads) once to find the place.  Collective.
 template <int kRows>
 __device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c, ScanMem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place r;
   long long mine = 0, sum = 0;
-  for (int b = tid; b < p.B; b += kThreads) sum += (mine = item_granules<kRows>(p, b));
+  for (int b = tid; b < p.B; b += kThreads) sum += (mine = item_cost<kRows>(p, keys_of(p, b)));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sm.sums[warp] = sum;
@@ -242,7 +248,7 @@ __device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c,
   long long before = 0;
   for (int base = 0; base < p.B; base += kThreads) {
     const int b = base + tid;
-    const long long n = p.B <= kThreads ? (b < p.B ? mine : 0) : (b < p.B ? item_granules<kRows>(p, b) : 0);
+    const long long n = p.B <= kThreads ? (b < p.B ? mine : 0) : (b < p.B ? item_cost<kRows>(p, keys_of(p, b)) : 0);
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -258,7 +264,7 @@ __device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c,
       if (w < warp) x += sm.sums[w];
       all += sm.sums[w];
     }
-    x += before;  // granules up to and with this item
+    x += before;  // cost up to and with this item
     if (want < x && want >= x - n) {
       sm.b = b;
       sm.off = want - (x - n);
@@ -272,27 +278,29 @@ __device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c,
   return r;
 }
 
-// The unit (row tile, KV head) that granule `off` of an item with len keys lies in, its granules, and the
-// granule's number inside it.
+// The unit (row tile, KV head) that `off` of the cost of an item with len keys lies in, its granules, and the
+// place inside it: r of its cost, where the fixed cost comes first, so granule max(0, r - over).
 struct Unit {
-  int tile, hk, n, g0;
+  int tile, hk, n, r, g0;
 };
 template <int kRows>
 __device__ __forceinline__ Unit unit_at(const AttParams& p, int len, long long off) {
   Unit u;
   for (u.tile = 0;; ++u.tile) {
     u.n = tile_granules<kRows>(p, len, u.tile);
-    const long long here = static_cast<long long>(u.n) * p.Hkv;
+    const long long here = u.n > 0 ? static_cast<long long>(u.n + p.over) * p.Hkv : 0;
     if (off < here) break;
     off -= here;
   }
+  const unsigned cost = u.n + p.over;
   if (off < (1LL << 31)) {
-    u.hk = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(u.n));
-    u.g0 = static_cast<int>(static_cast<unsigned>(off) % static_cast<unsigned>(u.n));
+    u.hk = static_cast<int>(static_cast<unsigned>(off) / cost);
+    u.r = static_cast<int>(static_cast<unsigned>(off) % cost);
   } else {
-    u.hk = static_cast<int>(off / u.n);
-    u.g0 = static_cast<int>(off % u.n);
+    u.hk = static_cast<int>(off / cost);
+    u.r = static_cast<int>(off % cost);
   }
+  u.g0 = max(0, u.r - p.over);
   return u;
 }
 
@@ -350,19 +358,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
 
   while (left > 0) {
     const int len = keys_of(p, b);
-    {
-      long long here = 0;
-      for (int i = 0; i < p.tiles; ++i) here += tile_granules<kRows>(p, len, i);
-      if (off >= here * p.Hkv) {  // (items without granules are passed over)
-        ++b;
-        off = 0;
-        continue;
-      }
+    if (off >= item_cost<kRows>(p, len)) {  // (items without granules are passed over)
+      ++b;
+      off = 0;
+      continue;
     }
     const Unit u = unit_at<kRows>(p, len, off);
-    const int take = static_cast<int>(min(left, static_cast<long long>(u.n - u.g0)));
-    left -= take;
-    off += take;
+    const int use = static_cast<int>(min(left, static_cast<long long>(u.n + p.over - u.r)));
+    const int take = max(0, u.r + use - p.over) - u.g0;
+    left -= use;
+    off += use;
+    if (take == 0) continue;  // a share that ends in the fixed cost of a unit leaves the unit to the next
     const int row0 = u.tile * kRows, hk = u.hk;
     const int tile_end = tile_keys<kRows>(p, len, u.tile), tile_all = row_limit(p, len, row0);
     const int lo = u.g0 * p.granule;
@@ -695,8 +701,8 @@ __global__ void __launch_bounds__(kThreads) kv8_combine_kernel(const AttParams p
   if (place.b < 0) return;
   const int shares = shares_of(p, place.total, grid);
   const Unit u = unit_at<kRows>(p, keys_of(p, place.b), place.off);
-  const long long here = share_begin(place.total, shares, c), begin = here - u.g0, end = begin + u.n;
-  if (u.g0 == 0 || begin < share_begin(place.total, shares, c - 1)) return;
+  const long long begin = share_begin(place.total, shares, c) - u.r, end = begin + u.n + p.over;
+  if (u.g0 == 0 || share_begin(place.total, shares, c - 1) > begin + p.over) return;
   int pieces = 1;  // beside the first
   while (c + pieces < shares && share_begin(place.total, shares, c + pieces) < end) ++pieces;
   auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + s)) * kRows; };
@@ -768,9 +774,10 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   p.ws_l = p.ws_o + static_cast<size_t>(2) * kCtas * R::kRows * D;
   const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
   p.granule = cap <= kShortKeys ? kShortKeys : kGranule;
+  p.over = p.granule == kGranule ? kUnitCost : 0;
   // no more CTAs than the fullest tables could give work to
-  const long long most = (cap + p.granule - 1) / p.granule * p.B * p.Hkv * p.tiles;
-  const int grid = static_cast<int>(std::min<long long>(kCtas, p.granule == kGranule ? (most + kMinGranules - 1) / kMinGranules : most));
+  const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
+  const int grid = static_cast<int>(std::min<long long>(kCtas, p.over ? (most + kMinShare - 1) / kMinShare : most));
   kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
   if (p.granule == kGranule && grid > 1) {
     // launched while the first kernel still runs: it finds its place meanwhile and waits for the pieces
