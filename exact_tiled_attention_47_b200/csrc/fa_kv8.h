@@ -75,11 +75,13 @@ struct PagesArgs {
   int* status;
 };
 
+size_t kv8_chunk_ws_bytes(int D);
 size_t kv8_attend_ws_bytes(int B, int Nq, int Hq, int Hkv, int D);
 size_t pages_ws_bytes(int n, int S, int num_pages);
 
 // Return a cudaError_t-compatible code (0 = success).
 int launch_kv8_append(const AppendArgs& a, cudaStream_t stream);
+int launch_kv8_chunk(const Attend8Args& a, cudaStream_t stream);  // many rows per KV head
 int launch_kv8_attend(const Attend8Args& a, cudaStream_t stream);
 int launch_pages_extend(const PagesArgs& a, cudaStream_t stream);
 int launch_pages_free(const PagesArgs& a, cudaStream_t stream);

@@ -33,7 +33,7 @@
 
 #include "fa_internal.h"
 #include "fa_kv8.h"
-#include "fa_prefill_common.cuh"
+#include "fa_kv8_sched.cuh"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -41,34 +41,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr float kLazy = 8.f;  // log2 units by which a maximum may be exceeded before it is raised
-constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that differences with -inf are defined)
-constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
-constexpr int kSms = 148;
-constexpr int kGranule = 64;      // keys: one block of 16 for each warp
-constexpr int kMinShare = 8;      // granules (a unit's fixed cost included) of a share: shorter ones cost more to merge than to read
-constexpr int kUnitCost = 4;      // granules that the fixed cost of a unit (queries, filling the ring, merging the warps) stands for
-constexpr int kShortKeys = 512;   // tables up to this many keys: a granule is a whole unit, and nothing is merged
-
-struct AttParams {
-  const void* q;
-  const uint8_t* k;
-  const uint8_t* v;
-  const float* ks;
-  const float* vs;
-  const int* table;
-  const int* seqlens;
-  void* o;
-  float* lse;
-  float* ws_o;  // [2 * shares, rows of a tile, D]: pieces of units
-  float* ws_l;  // [2 * shares, rows of a tile]
-  int B, Nq, Hq, Hkv, group, tiles;
-  int granule;  // keys
-  int over;     // kUnitCost, or 0 where a granule is a whole unit
-  int num_pages, page_shift, pps;
-  float scale_log2;
-  int* status;
-};
+constexpr int kGranule = 64;  // keys: one block of 16 for each warp
+constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (64 rows: 76 us here and 95 there,
+                               // 128 rows: 75 and 65; B8, 8 KV heads, D 128, 4096 and 2048 keys)
 
 // CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.  Four of
 // one group leave 128 registers and less overlap inside a warp: 200 us where three take 193 (4 x 131072).
@@ -163,155 +138,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return r;
 }
 
-// 2^e as fp32, e in [-126, 127].
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
-template <bool kFp16>
-__device__ __forceinline__ void store2(void* o, size_t at, float a, float b, bool f32) {
-  if (f32) *reinterpret_cast<float2*>(static_cast<float*>(o) + at) = make_float2(a, b);
-  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o) + at) = pack2<kFp16>(a, b);
-}
-
-// Keys of batch item b (0 for a length outside its range).
-__device__ __forceinline__ int keys_of(const AttParams& p, int b) {
-  const int cap = p.pps << p.page_shift;
-  if (!p.seqlens) return cap;
-  const int len = __ldg(p.seqlens + b);
-  return len < 0 || len > cap ? 0 : len;
-}
-
-// Keys that a row sees (rows of a token see the same ones), and granules of a row tile.
-__device__ __forceinline__ int row_limit(const AttParams& p, int len, int row) { return max(0, len - p.Nq + row / p.group + 1); }
-template <int kRows>
-__device__ __forceinline__ int tile_keys(const AttParams& p, int len, int tile) {
-  return row_limit(p, len, min(p.Nq * p.group, (tile + 1) * kRows) - 1);
-}
-template <int kRows>
-__device__ __forceinline__ int tile_granules(const AttParams& p, int len, int tile) {
-  return (tile_keys<kRows>(p, len, tile) + p.granule - 1) / p.granule;
-}
-// Cost of an item: the granules of its units and the units' fixed costs (a unit without granules has none).
-template <int kRows>
-__device__ __forceinline__ long long item_cost(const AttParams& p, int len) {
-  long long n = 0;
-  for (int i = 0; i < p.tiles; ++i) {
-    const int m = tile_granules<kRows>(p, len, i);
-    n += m > 0 ? m + p.over : 0;
-  }
-  return n * p.Hkv;
-}
-
-// Where a share begins: item b, `off` of the item's cost.
-struct Place {
-  long long total;  // cost of all items
-  long long off;
-  int b;
-};
-
-struct ScanMem {
-  long long sums[kWarps];
-  long long off;
-  int b;
-};
-
-// Number of shares of a total cost, and where share c begins.
-__device__ __forceinline__ int shares_of(const AttParams& p, long long total, int grid) {
-  const int least = p.over ? kMinShare : 1;
-  return static_cast<int>(min(static_cast<long long>(grid), (total + least - 1) / least));
-}
-__device__ __forceinline__ long long share_begin(long long total, int shares, int c) {
-  if (total < (1LL << 31)) {  // (a 64-bit division takes a hundred instructions)
-    const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(shares), r = static_cast<unsigned>(total) % static_cast<unsigned>(shares);
-    return static_cast<long long>(q) * c + min(c, static_cast<int>(r));
-  }
-  return total / shares * c + min(static_cast<long long>(c), total % shares);
-}
-
-// The place where share c begins: a scan of the items' costs, a CTA's worth at a time, once
-// for the total and (with more items than threads) once to find the place.  Collective.
-template <int kRows>
-__device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c, ScanMem& sm) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Place r;
-  long long mine = 0, sum = 0;
-  for (int b = tid; b < p.B; b += kThreads) sum += (mine = item_cost<kRows>(p, keys_of(p, b)));
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sm.sums[warp] = sum;
-  __syncthreads();
-  r.total = sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3];
-  const int shares = shares_of(p, r.total, grid);
-  r.b = -1;
-  r.off = 0;
-  if (c >= shares) return r;  // uniform: this CTA has no share
-  const long long want = share_begin(r.total, shares, c);
-  long long before = 0;
-  for (int base = 0; base < p.B; base += kThreads) {
-    const int b = base + tid;
-    const long long n = p.B <= kThreads ? (b < p.B ? mine : 0) : (b < p.B ? item_cost<kRows>(p, keys_of(p, b)) : 0);
-    long long x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();  // sums were read
-    if (lane == 31) sm.sums[warp] = x;
-    __syncthreads();
-    long long all = before;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) x += sm.sums[w];
-      all += sm.sums[w];
-    }
-    x += before;  // cost up to and with this item
-    if (want < x && want >= x - n) {
-      sm.b = b;
-      sm.off = want - (x - n);
-    }
-    before = all;
-    if (want < all) break;  // uniform
-  }
-  __syncthreads();
-  r.b = sm.b;
-  r.off = sm.off;
-  return r;
-}
-
-// The unit (row tile, KV head) that `off` of the cost of an item with len keys lies in, its granules, and the
-// place inside it: r of its cost, where the fixed cost comes first, so granule max(0, r - over).
-struct Unit {
-  int tile, hk, n, r, g0;
-};
-template <int kRows>
-__device__ __forceinline__ Unit unit_at(const AttParams& p, int len, long long off) {
-  Unit u;
-  for (u.tile = 0;; ++u.tile) {
-    u.n = tile_granules<kRows>(p, len, u.tile);
-    const long long here = u.n > 0 ? static_cast<long long>(u.n + p.over) * p.Hkv : 0;
-    if (off < here) break;
-    off -= here;
-  }
-  const unsigned cost = u.n + p.over;
-  if (off < (1LL << 31)) {
-    u.hk = static_cast<int>(static_cast<unsigned>(off) / cost);
-    u.r = static_cast<int>(static_cast<unsigned>(off) % cost);
-  } else {
-    u.hk = static_cast<int>(off / cost);
-    u.r = static_cast<int>(off % cost);
-  }
-  u.g0 = max(0, u.r - p.over);
-  return u;
-}
-
-// Index of a row among the rows of O [B, Nq, Hq, D], and of its LSE [B, Hq, Nq].
-__device__ __forceinline__ size_t o_row(const AttParams& p, int b, int hk, int row) {
-  return (static_cast<size_t>(b) * p.Nq + row / p.group) * p.Hq + hk * p.group + row % p.group;
-}
-__device__ __forceinline__ size_t lse_row(const AttParams& p, int b, int hk, int row) {
-  return (static_cast<size_t>(b) * p.Hq + hk * p.group + row % p.group) * p.Nq + row / p.group;
-}
-
 template <bool kFp16, bool kInt8, int D, int NG>
 __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const AttParams p, const int o_fp32) {
   using R = Ring<D, NG>;
@@ -320,60 +146,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
   constexpr int MT = D / 16;  // 16-column tiles of O (M of the second product)
   constexpr int kDShift = D == 128 ? 7 : 6;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ ScanMem scan;
+  __shared__ ScanMem<kThreads> scan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rows = p.Nq * p.group;
   const long long outs = static_cast<long long>(p.B) * p.Nq * p.Hq;
   const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
 
-  // rows of tiles that see no key at all, and lengths out of range (reported)
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (p.seqlens && tid == 0) {
-      const int len = __ldg(p.seqlens + b);
-      if (len < 0 || len > (p.pps << p.page_shift)) record_status(p.status, kStatusCuSeqlens);
-    }
-    const int len = keys_of(p, b);
-    for (int tile = 0; tile < p.tiles && tile_keys<kRows>(p, len, tile) == 0; ++tile) {
-      const int n = min(rows - tile * kRows, kRows) * p.Hkv;
-      for (int i = tid; i < n * (D / 2); i += kThreads) {
-        const int row = tile * kRows + i / (D / 2) / p.Hkv, hk = i / (D / 2) % p.Hkv, d = i % (D / 2) * 2;
-        const size_t at = o_row(p, b, hk, row);
-        if (!idx_ok(p.status, at, 1, outs)) continue;
-        store2<kFp16>(p.o, at * D + d, 0.f, 0.f, o_fp32 != 0);
-        if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
-      }
-    }
-  }
-
+  write_tiles_without_keys<kFp16, D, kRows>(p, o_fp32);
   asm volatile("griddepcontrol.launch_dependents;");
-  const Place place = find_place<kRows>(p, gridDim.x, blockIdx.x, scan);
+  const Place place = find_place<kRows, kThreads>(p, gridDim.x, blockIdx.x, scan);
   if (place.b < 0) return;
-  const int shares = shares_of(p, place.total, gridDim.x);
-  long long left = share_begin(place.total, shares, blockIdx.x + 1) - share_begin(place.total, shares, blockIdx.x);
-  long long off = place.off;
-  int b = place.b;
+  Walk walk = walk_of(p, place, gridDim.x, blockIdx.x);
 
   const uint32_t ring = smem_addr(smem) + warp * R::kWarp, ring_s = ring + kStages * R::kStage;
 
-  while (left > 0) {
-    const int len = keys_of(p, b);
-    if (off >= item_cost<kRows>(p, len)) {  // (items without granules are passed over)
-      ++b;
-      off = 0;
-      continue;
-    }
-    const Unit u = unit_at<kRows>(p, len, off);
-    const int use = static_cast<int>(min(left, static_cast<long long>(u.n + p.over - u.r)));
-    const int take = max(0, u.r + use - p.over) - u.g0;
-    left -= use;
-    off += use;
-    if (take == 0) continue;  // a share that ends in the fixed cost of a unit leaves the unit to the next
-    const int row0 = u.tile * kRows, hk = u.hk;
-    const int tile_end = tile_keys<kRows>(p, len, u.tile), tile_all = row_limit(p, len, row0);
-    const int lo = u.g0 * p.granule;
-    const int hi = static_cast<int>(min(static_cast<long long>(tile_end), static_cast<long long>(lo) + static_cast<long long>(take) * p.granule));
-    const bool whole = u.g0 == 0 && take == u.n;
+  Piece pc;
+  while (next_piece<kRows>(p, walk, pc)) {
+    const int b = pc.b, hk = pc.hk, row0 = pc.row0, len = pc.len, lo = pc.lo, hi = pc.hi;
+    const bool whole = pc.whole;
+    const int tile_all = row_limit(p, len, row0);  // keys that every row of the tile sees
 
     // the first blocks are on their way before the queries are read
     const int blocks = ((hi - lo + kKv8Block - 1) / kKv8Block - warp + kWarps - 1) / kWarps;
@@ -636,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
               make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
       }
     __syncthreads();
-    const int slot = 2 * blockIdx.x + (u.g0 == 0 ? 1 : 0);  // of a piece
+    const int slot = 2 * blockIdx.x + pc.slot;
     if (tid < kRows && row0 + tid < rows) {
       const int rr = row0 + tid;
       float M = kNone, W = kNone, sum = 0.f;
@@ -687,71 +479,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
   }
 }
 
-// Merges the pieces of the units that lie in more than one share.  CTA i looks at the border between
-// shares i and i + 1 and takes the unit it cuts, if no earlier border cuts the same one: piece 0 is the
-// end of share i, the others are the beginnings of shares i + 1, i + 2, ...  O = sum_s exp(lse_s - M) o_s /
-// sum_s exp(lse_s - M), LSE = M + ln of that sum; one warp per row.
-template <bool kFp16, int D, int NG>
-__global__ void __launch_bounds__(kThreads) kv8_combine_kernel(const AttParams p, const int o_fp32, const int grid) {
-  constexpr int kRows = 8 * NG, PER = D / 32, RPW = 2 * NG;  // rows of a warp, all under way at once
-  __shared__ ScanMem scan;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + 1;
-  const Place place = find_place<kRows>(p, grid, c, scan);
-  if (place.b < 0) return;
-  const int shares = shares_of(p, place.total, grid);
-  const Unit u = unit_at<kRows>(p, keys_of(p, place.b), place.off);
-  const long long begin = share_begin(place.total, shares, c) - u.r, end = begin + u.n + p.over;
-  if (u.g0 == 0 || share_begin(place.total, shares, c - 1) > begin + p.over) return;
-  int pieces = 1;  // beside the first
-  while (c + pieces < shares && share_begin(place.total, shares, c + pieces) < end) ++pieces;
-  auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + s)) * kRows; };
-  const int rows = min(kRows, p.Nq * p.group - u.tile * kRows);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-
-  float M[RPW], sum[RPW], acc[RPW][PER];
-#pragma unroll
-  for (int i = 0; i < RPW; ++i) {
-    M[i] = kNone;
-    sum[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
-  }
-  for (int s = 0; s <= pieces; ++s)
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int row = warp + i * kWarps;
-      if (row < rows) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
-    }
-  for (int s = 0; s <= pieces; ++s)
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int row = warp + i * kWarps;
-      if (row >= rows) continue;
-      const float w = ex2(p.ws_l[slot(s) + row] * kLog2e - M[i]);
-      sum[i] += w;
-      const float2* x = reinterpret_cast<const float2*>(p.ws_o + (slot(s) + row) * D) + lane * (PER / 2);
-#pragma unroll
-      for (int e = 0; e < PER / 2; ++e) {
-        const float2 y = x[e];
-        acc[i][2 * e] = fmaf(w, y.x, acc[i][2 * e]);
-        acc[i][2 * e + 1] = fmaf(w, y.y, acc[i][2 * e + 1]);
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < RPW; ++i) {
-    const int row = warp + i * kWarps, rr = u.tile * kRows + row;
-    if (row >= rows) continue;
-    const bool none = M[i] == kNone;
-    const float inv = none ? 0.f : 1.f / sum[i];
-    const size_t at = o_row(p, place.b, u.hk, rr);
-    if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
-#pragma unroll
-    for (int e = 0; e < PER / 2; ++e)
-      store2<kFp16>(p.o, at * D + lane * PER + 2 * e, acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv, o_fp32 != 0);
-    if (lane == 0) p.lse[lse_row(p, place.b, u.hk, rr)] = none ? -INFINITY : (M[i] + lg2(sum[i])) * kLn2;
-  }
-}
+// Which kernel takes a call, by its rows per KV head.
+bool on_chunk_kernel(int Nq, int group) { return static_cast<long long>(Nq) * group > kWarpRows; }
 
 // Rows of a tile, in groups of eight: as many tiles as 32 rows each take, of even size.
 int groups_for(int Nq, int group) {
@@ -779,20 +508,8 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
   const int grid = static_cast<int>(std::min<long long>(kCtas, p.over ? (most + kMinShare - 1) / kMinShare : most));
   kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
-  if (p.granule == kGranule && grid > 1) {
-    // launched while the first kernel still runs: it finds its place meanwhile and waits for the pieces
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kFp16, D, NG>, static_cast<const AttParams&>(p), static_cast<int>(a.o_fp32), grid);
-    if (e != cudaSuccess) return static_cast<int>(e);
-  }
+  if (p.over && grid > 1)
+    if (const int e = launch_combine8<kFp16, D, R::kRows>(p, a.o_fp32, grid, stream)) return e;
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -809,32 +526,14 @@ int launch_rows(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t kv8_attend_ws_bytes(int B, int Nq, int Hq, int Hkv, int D) {
+  if (on_chunk_kernel(Nq, Hq / Hkv)) return kv8_chunk_ws_bytes(D);
   const int n = groups_for(Nq, Hq / Hkv), per_sm = n == 1 ? kPerSm<1> : n == 2 ? kPerSm<2> : n == 3 ? kPerSm<3> : kPerSm<4>;
   return static_cast<size_t>(2) * per_sm * kSms * 8 * n * (D + 1) * sizeof(float);
 }
 
 int launch_kv8_attend(const Attend8Args& a, cudaStream_t stream) {
-  AttParams p;
-  p.q = a.q;
-  p.k = static_cast<const uint8_t*>(a.c.k);
-  p.v = static_cast<const uint8_t*>(a.c.v);
-  p.ks = a.c.ks;
-  p.vs = a.c.vs;
-  p.table = a.c.table;
-  p.seqlens = a.c.seqlens;
-  p.o = a.o;
-  p.lse = a.lse;
-  p.B = a.c.B;
-  p.Nq = a.Nq;
-  p.Hq = a.Hq;
-  p.Hkv = a.c.Hkv;
-  p.group = a.Hq / a.c.Hkv;
-  p.num_pages = a.c.num_pages;
-  p.page_shift = 0;
-  while ((1 << p.page_shift) < a.c.page_size) ++p.page_shift;
-  p.pps = a.c.pages_per_seq;
-  p.scale_log2 = a.scale * kLog2e;
-  p.status = a.status;
+  if (on_chunk_kernel(a.Nq, a.Hq / a.c.Hkv)) return launch_kv8_chunk(a, stream);
+  AttParams p = params_of(a);
   if (a.c.D == 64) {
     if (a.c.int8) return a.fp16 ? launch_rows<true, true, 64>(a, p, stream) : launch_rows<false, true, 64>(a, p, stream);
     return a.fp16 ? launch_rows<true, false, 64>(a, p, stream) : launch_rows<false, false, 64>(a, p, stream);

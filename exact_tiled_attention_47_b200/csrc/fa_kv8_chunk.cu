@@ -1,0 +1,606 @@
+// fa_kv8_chunk.cu -- attention over the paged 8-bit cache for many query rows per KV head (chunks of prompts,
+// long drafts): the mathematics of fa_kv8_attend.cu on tcgen05 tensor cores.
+//
+// The scheme is that of the prefill kernel (fa_prefill_sm100.cu): two 128-row Q tiles per CTA, a softmax
+// warpgroup and an MMA-issuing thread each, S and O in tensor memory, P in shared memory as the A operand of
+// P V, S(j+1) issued as soon as S(j) is in registers.  What differs:
+//   - K and V tiles are made by a warpgroup of its own: it loads the codes of 128 keys from their pages with
+//     16-byte loads one tile ahead, converts them to fp16 (exact) and stores them where TMA would have put
+//     them (128-byte rows, 16-byte chunks XOR-ed with the row).  It also brings the queries to fp16 (bf16
+//     rows times a power of two) and the scales to shared memory.
+//   - a tile has eight blocks of 16 keys with a scale each.  With f = q scale * ks and the maxima m (of the
+//     scores) and mo (of score + log2 vs), a weight is w = 2^(s f + log2 vs - mo): one fma and one ex2 as
+//     before, with other constants for each block; the row sum takes it back to 2^(s f - m) with the factor
+//     2^(mo - m - log2 vs) in the same instruction that adds it.  Where a block's vs is 2^64 or more below
+//     the row's largest contribution, that factor could meet a weight that was flushed to zero: then the
+//     row sums of the tile are computed from exponentials of their own.
+//   - the grid is one CTA per SM and shares the work evenly (fa_kv8_sched.cuh), pieces of cut units are
+//     merged by a second kernel.
+// Tensor memory: S0 S1 [0, 256), O0 O1 [256, 256 + 2 D).  Warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: MMA
+// issue (10 and 11 idle); 12-15: conversion.  16 warps leave the softmax 160 registers a thread, so a row of S is never
+// held as a whole: its two halves are read for the maxima, the second is turned into weights, the first is read again.
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "fa_kv8.h"
+#include "fa_kv8_sched.cuh"
+#include "fa_prefill_common.cuh"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kBM = 128;          // rows of a tile
+constexpr int kBN = 128;          // keys of a block
+constexpr int kUnitRows = 2 * kBM;
+constexpr int kChunkThreads = 512;
+constexpr int kMmaWarp = 8;       // owns TMEM; issues the MMAs of tile 0 (warp 9 those of tile 1)
+constexpr int kConvWarp = 12;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kPanelBytes = kBM * 128;  // 64 fp16 columns of a tile
+constexpr int kChunkUnitCost = 3;       // blocks that the fixed cost of a unit stands for
+// Registers: launched with kLaunchRegs per thread; the MMA warpgroup gives some to the two of the softmax.  The
+// sum must not exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms the
+// launch allocation once per device.
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 160;
+constexpr int kControlRegs = 64;
+static_assert(2 * kSoftmaxRegs + kControlRegs + kLaunchRegs <= 4 * kLaunchRegs, "register split");
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kPBytes = kBM * kBN * 2;
+  // D = 128 has room for one K and two V stages beside Q and P (K_{j+1} is needed a whole step after S(j))
+  static constexpr int kKStages = D == 64 ? 2 : 1;
+  static constexpr int kVStages = 2;
+  static constexpr int kKOff = 2 * kTileBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kPOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kBarOff = kPOff + 2 * kPBytes;
+  static constexpr int kSmemBytes = kBarOff + 2048 + 1024;  // barriers, scales; alignment slack
+  __device__ static constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
+  __device__ static constexpr uint32_t col_o(int t) { return 256u + (t ? static_cast<uint32_t>(D) : 0u); }
+};
+static_assert(ChunkCfg<64>::kSmemBytes <= 232448 && ChunkCfg<128>::kSmemBytes <= 232448, "shared memory budget");
+
+struct ChunkBars {
+  uint64_t q_full;
+  uint64_t k_full[2], v_full[2];
+  uint64_t k_empty[2][2], v_empty[2][2];  // [tile][stage]
+  uint64_t s_full[2], s_free[2], p_full[2], o_done[2], drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+  float2 scale[4][8];       // (ks, log2 vs) of the eight blocks of key block n % 4
+  signed char qexp[2][kUnitRows];  // the rows of piece s % 2 were multiplied by 2^-qexp
+  ScanMem<kChunkThreads> scan;
+};
+static_assert(sizeof(ChunkBars) <= 2048, "barrier block too large");
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Address of 16-byte chunk ch (8 columns) of row r of a tile of 64-column panels, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int ch) {
+  return base + (ch >> 3) * kPanelBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+
+// Four codes as two fp16 pairs in memory order.
+template <bool kInt8>
+__device__ __forceinline__ void halves_in_order(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kInt8) {
+    w ^= 0x80808080u;
+    lo = __byte_perm(w, 0x64646464u, 0x4140);
+    hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&lo), off), y = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+  }
+}
+
+// Weights of columns 32 ch ... 32 ch + 31 of 64 (two blocks of keys) of a row, their share of the row sum, packed to fp16.
+// kOwnSum: the row sum from exponentials of its own (see above).
+template <int kEmu, bool kOwnSum>
+__device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, const float2* scale, float qs, float m, float mo, uint64_t& acc0,
+                                          uint64_t& acc1, uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 sc = scale[h];
+    const float f = fmaxf(qs * sc.x, 1.17549435e-38f), e = sc.y - mo;
+    const float d = kOwnSum ? 1.f : ex2(mo - m - sc.y);
+    const uint64_t f2v = f2(f, f), e2v = f2(e, e), d2v = f2(d, d), m2v = f2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = ch * 32 + h * 16 + 2 * i;
+      const uint64_t s2 = f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+      const uint64_t x = f2_fma(s2, f2v, e2v);
+      uint64_t pe;
+      float x0, x1;
+      if ((i % kEmuEvery) < kEmu) {
+        pe = exp2_poly_pair(x);
+      } else {
+        f2_split(x, x0, x1);
+        pe = f2(ex2(x0), ex2(x1));
+      }
+      if constexpr (kOwnSum) {
+        f2_split(f2_fma(s2, f2v, m2v), x0, x1);
+        acc0 = f2_add(acc0, f2(ex2(x0), ex2(x1)));
+      } else if (i & 1) {
+        acc1 = f2_fma(pe, d2v, acc1);
+      } else {
+        acc0 = f2_fma(pe, d2v, acc0);
+      }
+      float p0, p1;
+      f2_split(pe, p0, p1);
+      pk[h * 8 + i] = pack2<true>(p0, p1);
+    }
+  }
+}
+
+template <bool kFp16, bool kInt8, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttParams p, const int o_fp32) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem + C::kBarOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = p.Nq * p.group;
+
+  write_tiles_without_keys<kFp16, D, kUnitRows>(p, o_fp32);
+  asm volatile("griddepcontrol.launch_dependents;");
+  const Place place = find_place<kUnitRows, kChunkThreads>(p, gridDim.x, blockIdx.x, bars->scan);
+  if (place.b < 0) return;  // uniform
+  Walk walk = walk_of(p, place, gridDim.x, blockIdx.x);
+  Piece pc;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->k_full[s], 4);
+      mbar_init(&bars->v_full[s], 4);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&bars->k_empty[t][s], 1);
+        mbar_init(&bars->v_empty[t][s], 1);
+      }
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_free[t], 4);
+      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->o_done[t], 1);
+      mbar_init(&bars->drain[t], 1);
+    }
+    bars->abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+  const uint32_t sQ = smem_addr(smem), sK = sQ + C::kKOff, sV = sQ + C::kVOff, sP = sQ + C::kPOff;
+  int n0 = 0;  // key blocks of the pieces before this one
+
+  if (warp >= kConvWarp) {
+    // ================================ conversion =================================================
+    const int cw = warp - kConvWarp;
+    const int r8 = lane >> 2, c4 = lane & 3;  // row of a group of eight, 16-code chunk of a 64-column panel
+    const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
+    bool ok = true;
+    for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
+      const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+      const int* table = p.table + static_cast<long long>(pc.b) * p.pps;
+      // Row of the pool where this warp's 16 keys [key0, key0 + 16) lie, -1 if there are none (a bad entry is
+      // reported: nothing is read through it).
+      auto pool_row = [&](int key0) -> long long {
+        if (key0 >= pc.hi) return -1;
+        const int page = __ldg(table + (key0 >> p.page_shift));
+        if (page < 0 || page >= p.num_pages) {
+          if (lane == 0) record_status(p.status, kStatusPageTable);
+          return -1;
+        }
+        const long long row = ((static_cast<long long>(page) * p.Hkv + pc.hk) << p.page_shift) + (key0 & ((1 << p.page_shift) - 1));
+        return idx_ok(p.status, row, kKv8Block, pool) ? row : -1;
+      };
+      long long row[2];            // of this warp's two blocks of 16 keys
+      uint4 kx[4][C::kPanels], vx[4][C::kPanels];
+      auto load = [&](const uint8_t* src, uint4 (&x)[4][C::kPanels], int key0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+            const long long at = row[i >> 1];
+            const int r = (i & 1) * 8 + r8;
+            x[i][pn] = make_uint4(0, 0, 0, 0);  // keys past the end: zeros
+            if (at >= 0 && key0 + i * 8 + r8 < pc.hi) x[i][pn] = __ldg(reinterpret_cast<const uint4*>(src + (at + r) * D + pn * 64 + c4 * 16));
+          }
+      };
+      auto store = [&](uint32_t tile, const uint4 (&x)[4][C::kPanels]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+            const uint32_t w[4] = {x[i][pn].x, x[i][pn].y, x[i][pn].z, x[i][pn].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) halves_in_order<kInt8>(w[k], h[2 * k], h[2 * k + 1]);
+            const int r = cw * 32 + i * 8 + r8, ch = pn * 8 + c4 * 2;
+            sts128(tile_at(tile, r, ch), h[0], h[1], h[2], h[3]);
+            sts128(tile_at(tile, r, ch + 1), h[4], h[5], h[6], h[7]);
+          }
+      };
+      float2 sc = make_float2(0.f, 0.f);  // lanes 0 and 1: scales of this warp's two blocks
+      auto fetch = [&](int j) {
+        const int key0 = pc.lo + j * kBN + cw * 32;
+        row[0] = pool_row(key0);
+        row[1] = pool_row(key0 + 16);
+        load(p.k, kx, key0);
+        if (lane < 2) {
+          const long long at = lane ? row[1] : row[0];
+          sc = make_float2(0.f, 1.f);  // (of a block behind the keys: any that is no extreme)
+          if (at >= 0) sc = make_float2(__ldg(p.ks + (at >> 4)), __ldg(p.vs + (at >> 4)));
+        }
+      };
+      fetch(0);
+      load(p.v, vx, pc.lo + cw * 32);
+
+      // the queries: the MMAs of the piece before must be done with theirs
+      if (n0 > 0) {
+        const int last = n0 - 1;
+        for (int t = 0; t < 2 && ok; ++t)
+          ok = warp_wait(&bars->k_empty[t][last % C::kKStages], (last / C::kKStages) & 1, abort_flag, p.status);
+        if (!ok) break;
+      }
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (pc.row0 + t * kBM >= rows) break;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int r = cw * 32 + i * 8 + r8, q = pc.row0 + t * kBM + r;
+          const bool in = q < rows;
+          const size_t at = o_row(p, pc.b, pc.hk, in ? q : pc.row0) * D + c4 * (D / 4);
+          uint32_t w[D / 8];
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const bool rd = in && idx_ok(p.status, at + 8 * k, 8, static_cast<long long>(p.B) * p.Nq * p.Hq * D);
+            const uint4 x = rd ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at) + k) : make_uint4(0, 0, 0, 0);
+            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+          }
+          int down = 0;
+          if constexpr (!kFp16) {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const float2 f = unpack2<false>(w[k]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 126);
+            const float up = pow2i(14 - e);
+            down = e - 14;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const float2 f = unpack2<false>(w[k]);
+              w[k] = pack2<true>(f.x * up, f.y * up);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            sts128(tile_at(sQ + t * C::kTileBytes, r, c4 * (D / 32) + k), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          if (c4 == 0) bars->qexp[s & 1][t * kBM + r] = static_cast<signed char>(down);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
+
+      for (int j = 0; j < blocks; ++j) {
+        const int n = n0 + j, ks = n % C::kKStages, vs = n % C::kVStages, ku = n / C::kKStages, vu = n / C::kVStages;
+        if (ku > 0) {
+          for (int t = 0; t < 2 && ok; ++t) ok = warp_wait(&bars->k_empty[t][ks], (ku - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+        }
+        store(sK + ks * C::kTileBytes, kx);
+        if (lane < 2) bars->scale[n & 3][cw * 2 + lane] = make_float2(sc.x, lg2(fmaxf(sc.y, 1.17549435e-38f)));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->k_full[ks]);
+        if (j + 1 < blocks) fetch(j + 1);
+        if (vu > 0) {
+          for (int t = 0; t < 2 && ok; ++t) ok = warp_wait(&bars->v_empty[t][vs], (vu - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+        }
+        store(sV + vs * C::kTileBytes, vx);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
+        if (j + 1 < blocks) load(p.v, vx, pc.lo + (j + 1) * kBN + cw * 32);
+      }
+      n0 += blocks;
+    }
+  } else if (warp >= 8) {
+    regs_decrease<kControlRegs>();
+    if (warp < kMmaWarp + 2 && lane == 0) {
+      // ================================ MMA issue ================================================
+      constexpr uint32_t idesc_qk = instr_desc_f16(kBM, kBN, 0, 0);
+      constexpr uint32_t idesc_pv = instr_desc_f16(kBM, D, 0, 1);
+      const int t = warp - kMmaWarp;
+      int c0 = 0;  // steps of this tile before this piece
+      bool ok = true;
+      for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
+        const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+        auto wait_k = [&](int j) {
+          const int n = n0 + j;
+          return mbar_wait(&bars->k_full[n % C::kKStages], (n / C::kKStages) & 1, abort_flag, p.status);
+        };
+        auto wait_v = [&](int j) {
+          const int n = n0 + j;
+          return mbar_wait(&bars->v_full[n % C::kVStages], (n / C::kVStages) & 1, abort_flag, p.status);
+        };
+        if (pc.row0 + t * kBM >= rows) {  // no such tile in this unit: its share of the stages is free at once
+          for (int j = 0; ok && j < blocks; ++j) {
+            if (!(ok = wait_k(j))) break;
+            mbar_arrive(&bars->k_empty[t][(n0 + j) % C::kKStages]);
+            if (!(ok = wait_v(j))) break;
+            mbar_arrive(&bars->v_empty[t][(n0 + j) % C::kVStages]);
+          }
+          n0 += blocks;
+          continue;
+        }
+        auto issue_s = [&](int j) {
+          const int st = (n0 + j) % C::kKStages;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
+            mma_ss(tbase + C::col_s(t), smem_desc_sw128(sQ + t * C::kTileBytes + off, 16, 1024),
+                   smem_desc_sw128(sK + st * C::kTileBytes + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars->s_full[t]);
+          mma_commit(&bars->k_empty[t][st]);
+        };
+        auto issue_pv = [&](int j) {
+          const int st = (n0 + j) % C::kVStages;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
+            mma_ss(tbase + C::col_o(t), smem_desc_sw128(sP + t * C::kPBytes + off, 16, 1024),
+                   smem_desc_sw128(sV + st * C::kTileBytes + kk * 2048, kPanelBytes, 1024), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(&bars->o_done[t]);
+          mma_commit(&bars->v_empty[t][st]);
+        };
+        if (!(ok = mbar_wait(&bars->q_full, s & 1, abort_flag, p.status) && wait_k(0))) break;
+        // the last scores of the piece before have been read
+        if (c0 > 0 && !(ok = mbar_wait(&bars->s_free[t], (c0 - 1) & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        issue_s(0);
+        for (int j = 0; j < blocks; ++j) {
+          if (j + 1 < blocks) {
+            if (!(ok = mbar_wait(&bars->s_free[t], (c0 + j) & 1, abort_flag, p.status) && wait_k(j + 1))) break;
+            tc_fence_after();
+            issue_s(j + 1);
+          }
+          if (!(ok = mbar_wait(&bars->p_full[t], (c0 + j) & 1, abort_flag, p.status) && wait_v(j))) break;
+          tc_fence_after();
+          issue_pv(j);
+        }
+        c0 += blocks;
+        n0 += blocks;
+      }
+      // no tensor-core work of this thread may still be in flight when TMEM and shared memory are released
+      mma_commit(&bars->drain[t]);
+      drain_wait(&bars->drain[t], 0);
+    }
+  } else {
+    regs_increase<kSoftmaxRegs>();
+    // ================================ softmax / epilogue =========================================
+    const int t = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t pbase = sP + t * C::kPBytes;
+    int c0 = 0;
+    bool ok = true;
+    for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
+      const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+      const int tile0 = pc.row0 + t * kBM, row = tile0 + r;
+      if (tile0 >= rows) {
+        n0 += blocks;
+        continue;
+      }
+      const int lim = row < rows ? min(row_limit(p, pc.len, row), pc.hi) : 0;  // keys below it are visible
+      const int all = tile0 + kBM <= rows ? min(row_limit(p, pc.len, tile0), pc.hi) : 0;  // to every row
+      float m = kNone, mo = kNone, qs = 0.f;
+      uint64_t lsum = f2(0.f, 0.f);
+      for (int j = 0; j < blocks; ++j) {
+        if (!(ok = warp_wait(&bars->s_full[t], (c0 + j) & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        if (j == 0) qs = p.scale_log2 * pow2i(bars->qexp[s & 1][t * kBM + r]);
+        const float2* scale = bars->scale[(n0 + j) & 3];
+        const int key0 = pc.lo + j * kBN;
+        const bool masked = key0 + kBN > all;
+        uint32_t sr[64];
+        auto read = [&](int half) {
+          tmem_ld64_sync(lane_base + C::col_s(t) + half * 64, sr);
+          if (masked) {
+            const int n = lim - key0 - half * 64;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= n) sr[c] = __float_as_uint(-INFINITY);
+          }
+        };
+        float mx = -INFINITY, mv = -INFINITY, lv_min = INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          read(half);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float2 sc = scale[half * 4 + h];
+            const int c = 16 * h;
+            float b0 = fmax3(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), __uint_as_float(sr[c + 2]));
+#pragma unroll
+            for (int i = 3; i < 15; i += 2) b0 = fmax3(b0, __uint_as_float(sr[c + i]), __uint_as_float(sr[c + i + 1]));
+            b0 = fmaxf(b0, __uint_as_float(sr[c + 15])) * fmaxf(qs * sc.x, 1.17549435e-38f);
+            mx = fmaxf(mx, b0);
+            mv = fmaxf(mv, b0 + sc.y);
+            lv_min = fminf(lv_min, sc.y);
+          }
+        }
+        // The maxima are raised when they are exceeded by more than 2^8 (warp-uniform); O waits below until
+        // the product before has landed.
+        const bool past = mx > m + kLazy || mv > mo + kLazy;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (__any_sync(0xffffffffu, past)) {
+          rescale = j > 0;
+          if (past) {
+            const float m_new = fmaxf(m, mx), mo_new = fmaxf(mo, mv), a = ex2(m - m_new);
+            alpha = ex2(mo - mo_new);
+            float l0, l1;
+            f2_split(lsum, l0, l1);
+            lsum = f2(l0 * a, l1 * a);
+            m = m_new;
+            mo = mo_new;
+          }
+        }
+        uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+        uint32_t pk[4][16];
+        const bool own = __any_sync(0xffffffffu, mo - m > lv_min + 64.f);
+        auto weigh = [&](int half) {
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            const float2* sc = scale + half * 4 + ch * 2;
+            uint32_t(&out)[16] = pk[half * 2 + ch];
+            if (own) weights32<0, true>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+            else if (masked) weights32<0, false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+            else weights32<1, false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+          }
+        };
+        weigh(1);
+        read(0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[t]);
+        weigh(0);
+        lsum = f2_add(lsum, f2_add(acc0, acc1));
+        if (j > 0) {
+          if (!(ok = warp_wait(&bars->o_done[t], (c0 + j - 1) & 1, abort_flag, p.status))) break;
+          tc_fence_after();
+        }
+        if (rescale) {
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t orr[32];
+            tmem_ld32_sync(lane_base + C::col_o(t) + ch * 32, orr);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha);
+            tmem_st32(lane_base + C::col_o(t) + ch * 32, orr);
+          }
+        }
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sts128(tile_at(pbase, r, ch * 4 + q), pk[ch][4 * q], pk[ch][4 * q + 1], pk[ch][4 * q + 2], pk[ch][4 * q + 3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (rescale) tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      if (!(ok = warp_wait(&bars->o_done[t], (c0 + blocks - 1) & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      c0 += blocks;
+      n0 += blocks;
+      float l0, l1;
+      f2_split(lsum, l0, l1);
+      const bool none = m == kNone;
+      const float f = none ? 0.f : ex2(mo - m) / (l0 + l1), ls = none ? -INFINITY : (m + lg2(l0 + l1)) * kLn2;
+      const int slot = 2 * blockIdx.x + pc.slot;
+      const size_t at = pc.whole ? o_row(p, pc.b, pc.hk, min(row, rows - 1)) : static_cast<size_t>(slot) * kUnitRows + t * kBM + r;
+      const bool st = row < rows && idx_ok(p.status, at, 1, pc.whole ? static_cast<long long>(p.B) * p.Nq * p.Hq : 2LL * gridDim.x * kUnitRows);
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t orr[32];
+        tmem_ld32_sync(lane_base + C::col_o(t) + ch * 32, orr);
+        const float* x = reinterpret_cast<const float*>(orr);
+        if (!st) continue;
+        if (!pc.whole || o_fp32) {
+          float4* out = reinterpret_cast<float4*>((pc.whole ? static_cast<float*>(p.o) : p.ws_o) + at * D + ch * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + at * D + ch * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            out[i] = make_uint4(pack2<kFp16>(x[8 * i] * f, x[8 * i + 1] * f), pack2<kFp16>(x[8 * i + 2] * f, x[8 * i + 3] * f),
+                                pack2<kFp16>(x[8 * i + 4] * f, x[8 * i + 5] * f), pack2<kFp16>(x[8 * i + 6] * f, x[8 * i + 7] * f));
+        }
+      }
+      tc_fence_before();  // O was read before the next piece's products are let go (by p_full)
+      if (st) (pc.whole ? p.lse[lse_row(p, pc.b, pc.hk, row)] : p.ws_l[at]) = ls;
+    }
+  }
+
+  // ---- teardown -------------------------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+template <bool kFp16, bool kInt8, int D>
+int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
+  auto kern = kv8_chunk_kernel<kFp16, kInt8, D>;
+  static PerContext<int> configured;
+  int unused = 0;
+  const int ce = configured.get(&unused, [&](int*) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    cudaFuncAttributes fattr;
+    e = cudaFuncGetAttributes(&fattr, kern);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    return fattr.numRegs == kLaunchRegs ? 0 : static_cast<int>(cudaErrorInvalidConfiguration);
+  });
+  if (ce != 0) return ce;
+  p.tiles = static_cast<int>((static_cast<long long>(a.Nq) * p.group + kUnitRows - 1) / kUnitRows);
+  p.ws_o = static_cast<float*>(a.ws);
+  p.ws_l = p.ws_o + static_cast<size_t>(2) * kSms * kUnitRows * D;
+  const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
+  p.granule = cap <= kShortKeys ? kShortKeys : kBN;
+  p.over = p.granule == kBN ? kChunkUnitCost : 0;
+  const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
+  const int grid = static_cast<int>(std::min<long long>(kSms, p.over ? (most + kMinShare - 1) / kMinShare : most));
+  kern<<<grid, kChunkThreads, ChunkCfg<D>::kSmemBytes, stream>>>(p, a.o_fp32);
+  if (p.over && grid > 1)
+    if (const int e = launch_combine8<kFp16, D, kUnitRows>(p, a.o_fp32, grid, stream)) return e;
+  return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+size_t kv8_chunk_ws_bytes(int D) { return static_cast<size_t>(2) * kSms * kUnitRows * (D + 1) * sizeof(float); }
+
+int launch_kv8_chunk(const Attend8Args& a, cudaStream_t stream) {
+  AttParams p = params_of(a);
+  if (a.c.D == 64) {
+    if (a.c.int8) return a.fp16 ? launch_t<true, true, 64>(a, p, stream) : launch_t<false, true, 64>(a, p, stream);
+    return a.fp16 ? launch_t<true, false, 64>(a, p, stream) : launch_t<false, false, 64>(a, p, stream);
+  }
+  if (a.c.int8) return a.fp16 ? launch_t<true, true, 128>(a, p, stream) : launch_t<false, true, 128>(a, p, stream);
+  return a.fp16 ? launch_t<true, false, 128>(a, p, stream) : launch_t<false, false, 128>(a, p, stream);
+}
+
+}  // namespace fa
