@@ -66,15 +66,25 @@ struct ChunkCfg {
 static_assert(ChunkCfg<64>::kSmemBytes <= 232448 && ChunkCfg<128>::kSmemBytes <= 232448, "shared memory budget");
 
 struct ChunkBars {
-  uint64_t q_full;
+  uint64_t q_full;   // `piece` is the next one, its queries are in place
+  uint64_t q_taken;  // every warp is done with `piece` (so that none falls a phase behind)
   uint64_t k_full[2], v_full[2];
   uint64_t k_empty[2][2], v_empty[2][2];  // [tile][stage]
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2], drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  float2 scale[4][8];       // (ks, log2 vs) of the eight blocks of key block n % 4
-  signed char qexp[2][kUnitRows];  // the rows of piece s % 2 were multiplied by 2^-qexp
-  ScanMem<kChunkThreads> scan;
+  // The pieces, walked by the conversion warps and handed on to the others (no keys left: the end).  With the walk in
+  // every warp's registers it was spilled into the inner loops, whose local memory misses the small L1 that the
+  // tiles leave: 938 us where this takes {CHUNK} (chunk of 1024 behind 16384 keys, B2).
+  Piece piece;
+  Walk walk[4];
+  union {
+    ScanMem<kChunkThreads> scan;  // before the roles part
+    struct {
+      float2 scale[4][8];              // (ks, log2 vs) of the eight blocks of key block n % 4
+      signed char qexp[2][kUnitRows];  // the rows of piece s % 2 were multiplied by 2^-qexp
+    };
+  };
 };
 static_assert(sizeof(ChunkBars) <= 2048, "barrier block too large");
 
@@ -105,7 +115,9 @@ __device__ __forceinline__ void halves_in_order(uint32_t w, uint32_t& lo, uint32
 
 // Weights of columns 32 ch ... 32 ch + 31 of 64 (two blocks of keys) of a row, their share of the row sum, packed to fp16.
 // kOwnSum: the row sum from exponentials of its own (see above).
-template <int kEmu, bool kOwnSum>
+// (The prefill's cubic for a part of the exponentials is off by up to 7.5e-5 relative: too much for the fp32 LSE of
+// a row that sees few keys, so all of them run on the MUFU here.)
+template <bool kOwnSum>
 __device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, const float2* scale, float qs, float m, float mo, uint64_t& acc0,
                                           uint64_t& acc1, uint32_t (&pk)[16]) {
 #pragma unroll
@@ -119,14 +131,10 @@ __device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, cons
       const int c = ch * 32 + h * 16 + 2 * i;
       const uint64_t s2 = f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
       const uint64_t x = f2_fma(s2, f2v, e2v);
-      uint64_t pe;
       float x0, x1;
-      if ((i % kEmuEvery) < kEmu) {
-        pe = exp2_poly_pair(x);
-      } else {
-        f2_split(x, x0, x1);
-        pe = f2(ex2(x0), ex2(x1));
-      }
+      f2_split(x, x0, x1);
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      const uint64_t pe = f2(p0, p1);
       if constexpr (kOwnSum) {
         f2_split(f2_fma(s2, f2v, m2v), x0, x1);
         acc0 = f2_add(acc0, f2(ex2(x0), ex2(x1)));
@@ -135,15 +143,13 @@ __device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, cons
       } else {
         acc0 = f2_fma(pe, d2v, acc0);
       }
-      float p0, p1;
-      f2_split(pe, p0, p1);
       pk[h * 8 + i] = pack2<true>(p0, p1);
     }
   }
 }
 
 template <bool kFp16, bool kInt8, int D>
-__global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttParams p, const int o_fp32) {
+__global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __grid_constant__ AttParams p, const int o_fp32) {
   using C = ChunkCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -155,11 +161,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
   asm volatile("griddepcontrol.launch_dependents;");
   const Place place = find_place<kUnitRows, kChunkThreads>(p, gridDim.x, blockIdx.x, bars->scan);
   if (place.b < 0) return;  // uniform
-  Walk walk = walk_of(p, place, gridDim.x, blockIdx.x);
-  Piece pc;
+  __syncthreads();  // scan and what lies in its place may be written
+  if (threadIdx.x < 4) bars->walk[threadIdx.x] = walk_of(p, place, gridDim.x, blockIdx.x);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 4);
+    mbar_init(&bars->q_taken, 10);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->k_full[s], 4);
       mbar_init(&bars->v_full[s], 4);
@@ -196,19 +203,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
     const int r8 = lane >> 2, c4 = lane & 3;  // row of a group of eight, 16-code chunk of a 64-column panel
     const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
     bool ok = true;
-    for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
-      const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+    for (int s = 0; ok; ++s) {
+      Piece pc;
+      bool more = false;
+      if (lane == 0) more = next_piece<kUnitRows>(p, bars->walk[cw], pc);
+      more = __shfl_sync(0xffffffffu, more, 0);
+      if (n0 > 0) {  // the MMAs of the piece before must be done with its queries
+        const int last = n0 - 1;
+        for (int t = 0; t < 2 && ok; ++t)
+          ok = warp_wait(&bars->k_empty[t][last % C::kKStages], (last / C::kKStages) & 1, abort_flag, p.status);
+      }
+      if (!ok) break;
+      // Hands the piece on.  Every warp waits for each phase of q_taken before it lets the next one begin.
+      auto publish = [&]() {
+        if (s > 0 && !warp_wait(&bars->q_taken, (s - 1) & 1, abort_flag, p.status)) return false;
+        if (cw == 0 && lane == 0) bars->piece = pc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+        return true;
+      };
+      if (!more) {
+        pc.lo = pc.hi = 0;
+        publish();
+        break;
+      }
+      pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
+      pc.row0 = __shfl_sync(0xffffffffu, pc.row0, 0);
+      const int hk = __shfl_sync(0xffffffffu, pc.hk, 0);
+      const int lo = __shfl_sync(0xffffffffu, pc.lo, 0), hi = __shfl_sync(0xffffffffu, pc.hi, 0), blocks = (hi - lo + kBN - 1) / kBN;
       const int* table = p.table + static_cast<long long>(pc.b) * p.pps;
       // Row of the pool where this warp's 16 keys [key0, key0 + 16) lie, -1 if there are none (a bad entry is
       // reported: nothing is read through it).
       auto pool_row = [&](int key0) -> long long {
-        if (key0 >= pc.hi) return -1;
+        if (key0 >= hi) return -1;
         const int page = __ldg(table + (key0 >> p.page_shift));
         if (page < 0 || page >= p.num_pages) {
           if (lane == 0) record_status(p.status, kStatusPageTable);
           return -1;
         }
-        const long long row = ((static_cast<long long>(page) * p.Hkv + pc.hk) << p.page_shift) + (key0 & ((1 << p.page_shift) - 1));
+        const long long row = ((static_cast<long long>(page) * p.Hkv + hk) << p.page_shift) + (key0 & ((1 << p.page_shift) - 1));
         return idx_ok(p.status, row, kKv8Block, pool) ? row : -1;
       };
       long long row[2];            // of this warp's two blocks of 16 keys
@@ -221,7 +254,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
             const long long at = row[i >> 1];
             const int r = (i & 1) * 8 + r8;
             x[i][pn] = make_uint4(0, 0, 0, 0);  // keys past the end: zeros
-            if (at >= 0 && key0 + i * 8 + r8 < pc.hi) x[i][pn] = __ldg(reinterpret_cast<const uint4*>(src + (at + r) * D + pn * 64 + c4 * 16));
+            if (at >= 0 && key0 + i * 8 + r8 < hi) x[i][pn] = __ldg(reinterpret_cast<const uint4*>(src + (at + r) * D + pn * 64 + c4 * 16));
           }
       };
       auto store = [&](uint32_t tile, const uint4 (&x)[4][C::kPanels]) {
@@ -240,7 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
       };
       float2 sc = make_float2(0.f, 0.f);  // lanes 0 and 1: scales of this warp's two blocks
       auto fetch = [&](int j) {
-        const int key0 = pc.lo + j * kBN + cw * 32;
+        const int key0 = lo + j * kBN + cw * 32;
         row[0] = pool_row(key0);
         row[1] = pool_row(key0 + 16);
         load(p.k, kx, key0);
@@ -251,15 +284,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         }
       };
       fetch(0);
-      load(p.v, vx, pc.lo + cw * 32);
+      load(p.v, vx, lo + cw * 32);
 
-      // the queries: the MMAs of the piece before must be done with theirs
-      if (n0 > 0) {
-        const int last = n0 - 1;
-        for (int t = 0; t < 2 && ok; ++t)
-          ok = warp_wait(&bars->k_empty[t][last % C::kKStages], (last / C::kKStages) & 1, abort_flag, p.status);
-        if (!ok) break;
-      }
+      // the queries
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         if (pc.row0 + t * kBM >= rows) break;
@@ -267,7 +294,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         for (int i = 0; i < 4; ++i) {
           const int r = cw * 32 + i * 8 + r8, q = pc.row0 + t * kBM + r;
           const bool in = q < rows;
-          const size_t at = o_row(p, pc.b, pc.hk, in ? q : pc.row0) * D + c4 * (D / 4);
+          const size_t at = o_row(p, pc.b, hk, in ? q : pc.row0) * D + c4 * (D / 4);
           uint32_t w[D / 8];
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
@@ -301,8 +328,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_full);
+      if (!(ok = publish())) break;
 
       for (int j = 0; j < blocks; ++j) {
         const int n = n0 + j, ks = n % C::kKStages, vs = n % C::kVStages, ku = n / C::kKStages, vu = n / C::kVStages;
@@ -324,7 +350,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->v_full[vs]);
-        if (j + 1 < blocks) load(p.v, vx, pc.lo + (j + 1) * kBN + cw * 32);
+        if (j + 1 < blocks) load(p.v, vx, lo + (j + 1) * kBN + cw * 32);
       }
       n0 += blocks;
     }
@@ -337,8 +363,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
       const int t = warp - kMmaWarp;
       int c0 = 0;  // steps of this tile before this piece
       bool ok = true;
-      for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
-        const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+      for (int s = 0; ok; ++s) {
+        if (!(ok = mbar_wait(&bars->q_full, s & 1, abort_flag, p.status))) break;
+        const int blocks = (bars->piece.hi - bars->piece.lo + kBN - 1) / kBN;
+        const bool mine = bars->piece.row0 + t * kBM < rows;
+        if (blocks == 0) break;
+        mbar_arrive(&bars->q_taken);
         auto wait_k = [&](int j) {
           const int n = n0 + j;
           return mbar_wait(&bars->k_full[n % C::kKStages], (n / C::kKStages) & 1, abort_flag, p.status);
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
           const int n = n0 + j;
           return mbar_wait(&bars->v_full[n % C::kVStages], (n / C::kVStages) & 1, abort_flag, p.status);
         };
-        if (pc.row0 + t * kBM >= rows) {  // no such tile in this unit: its share of the stages is free at once
+        if (!mine) {  // no such tile in this unit: its share of the stages is free at once
           for (int j = 0; ok && j < blocks; ++j) {
             if (!(ok = wait_k(j))) break;
             mbar_arrive(&bars->k_empty[t][(n0 + j) % C::kKStages]);
@@ -379,7 +409,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
           mma_commit(&bars->o_done[t]);
           mma_commit(&bars->v_empty[t][st]);
         };
-        if (!(ok = mbar_wait(&bars->q_full, s & 1, abort_flag, p.status) && wait_k(0))) break;
+        if (!(ok = wait_k(0))) break;
         // the last scores of the piece before have been read
         if (c0 > 0 && !(ok = mbar_wait(&bars->s_free[t], (c0 - 1) & 1, abort_flag, p.status))) break;
         tc_fence_after();
@@ -410,11 +440,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
     const uint32_t pbase = sP + t * C::kPBytes;
     int c0 = 0;
     bool ok = true;
-    for (int s = 0; ok && next_piece<kUnitRows>(p, walk, pc); ++s) {
-      const int blocks = (pc.hi - pc.lo + kBN - 1) / kBN;
+    for (int s = 0; ok; ++s) {
+      if (!(ok = warp_wait(&bars->q_full, s & 1, abort_flag, p.status))) break;
+      const Piece& pc = bars->piece;
+      const int lo = pc.lo, blocks = (pc.hi - lo + kBN - 1) / kBN;
+      if (blocks == 0) break;
       const int tile0 = pc.row0 + t * kBM, row = tile0 + r;
       if (tile0 >= rows) {
         n0 += blocks;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_taken);
         continue;
       }
       const int lim = row < rows ? min(row_limit(p, pc.len, row), pc.hi) : 0;  // keys below it are visible
@@ -426,7 +461,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         tc_fence_after();
         if (j == 0) qs = p.scale_log2 * pow2i(bars->qexp[s & 1][t * kBM + r]);
         const float2* scale = bars->scale[(n0 + j) & 3];
-        const int key0 = pc.lo + j * kBN;
+        const int key0 = lo + j * kBN;
         const bool masked = key0 + kBN > all;
         uint32_t sr[64];
         auto read = [&](int half) {
@@ -480,9 +515,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
           for (int ch = 0; ch < 2; ++ch) {
             const float2* sc = scale + half * 4 + ch * 2;
             uint32_t(&out)[16] = pk[half * 2 + ch];
-            if (own) weights32<0, true>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
-            else if (masked) weights32<0, false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
-            else weights32<1, false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+            if (own) weights32<true>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+            else weights32<false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
           }
         };
         weigh(1);
@@ -534,8 +568,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
         uint32_t orr[32];
         tmem_ld32_sync(lane_base + C::col_o(t) + ch * 32, orr);
         const float* x = reinterpret_cast<const float*>(orr);
-        if (!st) continue;
-        if (!pc.whole || o_fp32) {
+        if (!st) {
+          // nothing of this row is stored (the loads of O are collective)
+        } else if (!pc.whole || o_fp32) {
           float4* out = reinterpret_cast<float4*>((pc.whole ? static_cast<float*>(p.o) : p.ws_o) + at * D + ch * 32);
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
@@ -549,6 +584,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttPa
       }
       tc_fence_before();  // O was read before the next piece's products are let go (by p_full)
       if (st) (pc.whole ? p.lse[lse_row(p, pc.b, pc.hk, row)] : p.ws_l[at]) = ls;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_taken);
     }
   }
 
