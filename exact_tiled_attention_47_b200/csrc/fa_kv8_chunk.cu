@@ -39,13 +39,14 @@ constexpr int kConvWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPanelBytes = kBM * 128;  // 64 fp16 columns of a tile
 constexpr int kChunkUnitCost = 3;       // blocks that the fixed cost of a unit stands for
-// Registers: launched with kLaunchRegs per thread; the MMA warpgroup gives some to the two of the softmax.  The
+// Registers: launched with kLaunchRegs per thread; the MMA and conversion warpgroups give some to the two of the softmax.  The
 // sum must not exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms the
 // launch allocation once per device.
 constexpr int kLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 160;
-constexpr int kControlRegs = 64;
-static_assert(2 * kSoftmaxRegs + kControlRegs + kLaunchRegs <= 4 * kLaunchRegs, "register split");
+constexpr int kSoftmaxRegs = 176;
+constexpr int kControlRegs = 40;
+constexpr int kConvRegs = 120;
+static_assert(2 * kSoftmaxRegs + kControlRegs + kConvRegs <= 4 * kLaunchRegs, "register split");
 
 template <int D>
 struct ChunkCfg {
@@ -90,6 +91,25 @@ static_assert(sizeof(ChunkBars) <= 2048, "barrier block too large");
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 16 bytes that this SM reads once: not kept in the little L1 that the tiles leave.
+__device__ __forceinline__ uint4 ldg_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// D (+)= A B with the operands' descriptors (smem_desc_sw128) as their low words, the high word is common: the
+// issuing thread shares its sub-partition with computing warps, so it gets few instructions per MMA.
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // Address of 16-byte chunk ch (8 columns) of row r of a tile of 64-column panels, 128-byte swizzle.
@@ -198,6 +218,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
   int n0 = 0;  // key blocks of the pieces before this one
 
   if (warp >= kConvWarp) {
+    regs_decrease<kConvRegs>();
     // ================================ conversion =================================================
     const int cw = warp - kConvWarp;
     const int r8 = lane >> 2, c4 = lane & 3;  // row of a group of eight, 16-code chunk of a 64-column panel
@@ -254,7 +275,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
             const long long at = row[i >> 1];
             const int r = (i & 1) * 8 + r8;
             x[i][pn] = make_uint4(0, 0, 0, 0);  // keys past the end: zeros
-            if (at >= 0 && key0 + i * 8 + r8 < hi) x[i][pn] = __ldg(reinterpret_cast<const uint4*>(src + (at + r) * D + pn * 64 + c4 * 16));
+            if (at >= 0 && key0 + i * 8 + r8 < hi) x[i][pn] = ldg_once(src + (at + r) * D + pn * 64 + c4 * 16);
           }
       };
       auto store = [&](uint32_t tile, const uint4 (&x)[4][C::kPanels]) {
@@ -283,10 +304,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
           if (at >= 0) sc = make_float2(__ldg(p.ks + (at >> 4)), __ldg(p.vs + (at >> 4)));
         }
       };
-      fetch(0);
-      load(p.v, vx, lo + cw * 32);
-
-      // the queries
+      // the queries (before the first codes are loaded: both at once would not fit the registers)
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         if (pc.row0 + t * kBM >= rows) break;
@@ -328,6 +346,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      fetch(0);
+      load(p.v, vx, lo + cw * 32);
       if (!(ok = publish())) break;
 
       for (int j = 0; j < blocks; ++j) {
@@ -361,6 +381,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       constexpr uint32_t idesc_qk = instr_desc_f16(kBM, kBN, 0, 0);
       constexpr uint32_t idesc_pv = instr_desc_f16(kBM, D, 0, 1);
       const int t = warp - kMmaWarp;
+      // low words of the operands' descriptors (K-major Q, K, P; V with its panels kPanelBytes apart)
+      const uint32_t q_lo = static_cast<uint32_t>(smem_desc_sw128(sQ + t * C::kTileBytes, 16, 1024)), k_lo = static_cast<uint32_t>(smem_desc_sw128(sK, 16, 1024));
+      const uint32_t p_lo = static_cast<uint32_t>(smem_desc_sw128(sP + t * C::kPBytes, 16, 1024)), v_lo = static_cast<uint32_t>(smem_desc_sw128(sV, kPanelBytes, 1024));
+      const uint32_t kDescHi = static_cast<uint32_t>(smem_desc_sw128(0, 16, 1024) >> 32);
       int c0 = 0;  // steps of this tile before this piece
       bool ok = true;
       for (int s = 0; ok; ++s) {
@@ -389,22 +413,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         }
         auto issue_s = [&](int j) {
           const int st = (n0 + j) % C::kKStages;
+          const uint32_t a = q_lo, b = k_lo + st * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
-            mma_ss(tbase + C::col_s(t), smem_desc_sw128(sQ + t * C::kTileBytes + off, 16, 1024),
-                   smem_desc_sw128(sK + st * C::kTileBytes + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {  // 16 columns are 32 bytes of a row, 64 a panel
+            const uint32_t off = ((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4;
+            mma_ss_lo(tbase + C::col_s(t), a + off, b + off, kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
           }
           mma_commit(&bars->s_full[t]);
           mma_commit(&bars->k_empty[t][st]);
         };
         auto issue_pv = [&](int j) {
           const int st = (n0 + j) % C::kVStages;
+          const uint32_t a = p_lo, b = v_lo + st * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
-            mma_ss(tbase + C::col_o(t), smem_desc_sw128(sP + t * C::kPBytes + off, 16, 1024),
-                   smem_desc_sw128(sV + st * C::kTileBytes + kk * 2048, kPanelBytes, 1024), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBN / 16; ++kk) {  // 16 keys are two 1024-byte atoms of V
+            const uint32_t off = ((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4;
+            mma_ss_lo(tbase + C::col_o(t), a + off, b + ((kk * 2048) >> 4), kDescHi, idesc_pv, kk > 0 ? 1u : (j > 0 ? 1u : 0u));
           }
           mma_commit(&bars->o_done[t]);
           mma_commit(&bars->v_empty[t][st]);
