@@ -17,7 +17,7 @@
 //   - the grid is one CTA per SM and shares the work evenly (fa_kv8_sched.cuh), pieces of cut units are
 //     merged by a second kernel.
 // Tensor memory: S0 S1 [0, 256), O0 O1 [256, 256 + 2 D).  Warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: MMA
-// issue (10 and 11 idle); 12-15: conversion.  16 warps leave the softmax 160 registers a thread, so a row of S is never
+// issue (10 and 11 idle); 12-15: conversion.  16 warps leave the softmax 168 registers a thread, so a row of S is never
 // held as a whole: its two halves are read for the maxima, the second is turned into weights, the first is read again.
 #include <algorithm>
 
@@ -43,8 +43,8 @@ constexpr int kChunkUnitCost = 3;       // blocks that the fixed cost of a unit 
 // sum must not exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms the
 // launch allocation once per device.
 constexpr int kLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 176;
-constexpr int kControlRegs = 40;
+constexpr int kSoftmaxRegs = 168;
+constexpr int kControlRegs = 56;
 constexpr int kConvRegs = 120;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kConvRegs <= 4 * kLaunchRegs, "register split");
 
@@ -67,8 +67,8 @@ struct ChunkCfg {
 static_assert(ChunkCfg<64>::kSmemBytes <= 232448 && ChunkCfg<128>::kSmemBytes <= 232448, "shared memory budget");
 
 struct ChunkBars {
-  uint64_t q_full;   // `piece` is the next one, its queries are in place
-  uint64_t q_taken;  // every warp is done with `piece` (so that none falls a phase behind)
+  uint64_t q_full;   // piece s is in piece[s % 2], its queries are in place
+  uint64_t q_taken;  // every warp is done with it (so that none falls a phase behind)
   uint64_t k_full[2], v_full[2];
   uint64_t k_empty[2][2], v_empty[2][2];  // [tile][stage]
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2], drain[2];
@@ -76,8 +76,8 @@ struct ChunkBars {
   int abort_flag;
   // The pieces, walked by the conversion warps and handed on to the others (no keys left: the end).  With the walk in
   // every warp's registers it was spilled into the inner loops, whose local memory misses the small L1 that the
-  // tiles leave: 938 us where this takes {CHUNK} (chunk of 1024 behind 16384 keys, B2).
-  Piece piece;
+  // tiles leave: 938 us where this takes 710 (chunk of 1024 behind 16384 keys, B2).
+  Piece piece[2];
   Walk walk[4];
   union {
     ScanMem<kChunkThreads> scan;  // before the roles part
@@ -133,16 +133,23 @@ __device__ __forceinline__ void halves_in_order(uint32_t w, uint32_t& lo, uint32
   }
 }
 
+// (ks, log2 vs) of block h of those whose pairs begin at this shared-memory address.
+__device__ __forceinline__ float2 scale_at(uint32_t scale, int h) {
+  float2 r;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(scale + h * 8));
+  return r;
+}
+
 // Weights of columns 32 ch ... 32 ch + 31 of 64 (two blocks of keys) of a row, their share of the row sum, packed to fp16.
 // kOwnSum: the row sum from exponentials of its own (see above).
 // (The prefill's cubic for a part of the exponentials is off by up to 7.5e-5 relative: too much for the fp32 LSE of
 // a row that sees few keys, so all of them run on the MUFU here.)
 template <bool kOwnSum>
-__device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, const float2* scale, float qs, float m, float mo, uint64_t& acc0,
+__device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, uint32_t scale, float qs, float m, float mo, uint64_t& acc0,
                                           uint64_t& acc1, uint32_t (&pk)[16]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float2 sc = scale[h];
+    const float2 sc = scale_at(scale, h);
     const float f = fmaxf(qs * sc.x, 1.17549435e-38f), e = sc.y - mo;
     const float d = kOwnSum ? 1.f : ex2(mo - m - sc.y);
     const uint64_t f2v = f2(f, f), e2v = f2(e, e), d2v = f2(d, d), m2v = f2(-m, -m);
@@ -226,9 +233,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
     bool ok = true;
     for (int s = 0; ok; ++s) {
       Piece pc;
-      bool more = false;
-      if (lane == 0) more = next_piece<kUnitRows>(p, bars->walk[cw], pc);
-      more = __shfl_sync(0xffffffffu, more, 0);
+      if (lane == 0) {
+        if (!next_piece<kUnitRows>(p, bars->walk[cw], pc)) pc.lo = pc.hi = 0;  // the end
+        if (cw == 0) bars->piece[s & 1] = pc;  // (piece s - 2 was taken before s - 1 was handed on)
+      }
       if (n0 > 0) {  // the MMAs of the piece before must be done with its queries
         const int last = n0 - 1;
         for (int t = 0; t < 2 && ok; ++t)
@@ -238,20 +246,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       // Hands the piece on.  Every warp waits for each phase of q_taken before it lets the next one begin.
       auto publish = [&]() {
         if (s > 0 && !warp_wait(&bars->q_taken, (s - 1) & 1, abort_flag, p.status)) return false;
-        if (cw == 0 && lane == 0) bars->piece = pc;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full);
         return true;
       };
-      if (!more) {
-        pc.lo = pc.hi = 0;
+      const int lo = __shfl_sync(0xffffffffu, pc.lo, 0), hi = __shfl_sync(0xffffffffu, pc.hi, 0), blocks = (hi - lo + kBN - 1) / kBN;
+      if (blocks == 0) {
         publish();
         break;
       }
       pc.b = __shfl_sync(0xffffffffu, pc.b, 0);
       pc.row0 = __shfl_sync(0xffffffffu, pc.row0, 0);
       const int hk = __shfl_sync(0xffffffffu, pc.hk, 0);
-      const int lo = __shfl_sync(0xffffffffu, pc.lo, 0), hi = __shfl_sync(0xffffffffu, pc.hi, 0), blocks = (hi - lo + kBN - 1) / kBN;
       const int* table = p.table + static_cast<long long>(pc.b) * p.pps;
       // Row of the pool where this warp's 16 keys [key0, key0 + 16) lie, -1 if there are none (a bad entry is
       // reported: nothing is read through it).
@@ -268,6 +274,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       long long row[2];            // of this warp's two blocks of 16 keys
       uint4 kx[4][C::kPanels], vx[4][C::kPanels];
       auto load = [&](const uint8_t* src, uint4 (&x)[4][C::kPanels], int key0) {
+        const int left = hi - key0 - r8;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
             const long long at = row[i >> 1];
             const int r = (i & 1) * 8 + r8;
             x[i][pn] = make_uint4(0, 0, 0, 0);  // keys past the end: zeros
-            if (at >= 0 && key0 + i * 8 + r8 < hi) x[i][pn] = ldg_once(src + (at + r) * D + pn * 64 + c4 * 16);
+            if (at >= 0 && i * 8 < left) x[i][pn] = ldg_once(src + (at + r) * D + pn * 64 + c4 * 16);
           }
       };
       auto store = [&](uint32_t tile, const uint4 (&x)[4][C::kPanels]) {
@@ -389,8 +396,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       bool ok = true;
       for (int s = 0; ok; ++s) {
         if (!(ok = mbar_wait(&bars->q_full, s & 1, abort_flag, p.status))) break;
-        const int blocks = (bars->piece.hi - bars->piece.lo + kBN - 1) / kBN;
-        const bool mine = bars->piece.row0 + t * kBM < rows;
+        const int blocks = (bars->piece[s & 1].hi - bars->piece[s & 1].lo + kBN - 1) / kBN;
+        const bool mine = bars->piece[s & 1].row0 + t * kBM < rows;
         if (blocks == 0) break;
         mbar_arrive(&bars->q_taken);
         auto wait_k = [&](int j) {
@@ -461,12 +468,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
     const int t = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t pbase = sP + t * C::kPBytes;
+    const uint32_t pbase = sP + t * C::kPBytes, scale0 = smem_addr(bars->scale);
     int c0 = 0;
     bool ok = true;
     for (int s = 0; ok; ++s) {
       if (!(ok = warp_wait(&bars->q_full, s & 1, abort_flag, p.status))) break;
-      const Piece& pc = bars->piece;
+      const Piece& pc = bars->piece[s & 1];
       const int lo = pc.lo, blocks = (pc.hi - lo + kBN - 1) / kBN;
       if (blocks == 0) break;
       const int tile0 = pc.row0 + t * kBM, row = tile0 + r;
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         if (!(ok = warp_wait(&bars->s_full[t], (c0 + j) & 1, abort_flag, p.status))) break;
         tc_fence_after();
         if (j == 0) qs = p.scale_log2 * pow2i(bars->qexp[s & 1][t * kBM + r]);
-        const float2* scale = bars->scale[(n0 + j) & 3];
+        const uint32_t scale = scale0 + ((n0 + j) & 3) * 64;  // of the block's eight pairs
         const int key0 = lo + j * kBN;
         const bool masked = key0 + kBN > all;
         uint32_t sr[64];
@@ -503,7 +510,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
           read(half);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const float2 sc = scale[half * 4 + h];
+            const float2 sc = scale_at(scale, half * 4 + h);
             const int c = 16 * h;
             float b0 = fmax3(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), __uint_as_float(sr[c + 2]));
 #pragma unroll
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         auto weigh = [&](int half) {
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
-            const float2* sc = scale + half * 4 + ch * 2;
+            const uint32_t sc = scale + (half * 4 + ch * 2) * 8;
             uint32_t(&out)[16] = pk[half * 2 + ch];
             if (own) weights32<true>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
             else weights32<false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
