@@ -9,24 +9,30 @@ from __future__ import annotations
 
 import contextlib
 import functools
-import math
 
 import exact_tiled_attention_47_b200 as fa
 
 from . import _lib
 from ._lib import load
 
-_CODES = None
-_FLOATS = None
+_TORCH = _INT32 = _FLOAT32 = _CODES = _FLOATS = None
+
+
+def _torch():
+    """torch, imported on first use as everywhere in the package; sets the types that the checks compare with."""
+    global _TORCH, _INT32, _FLOAT32, _CODES, _FLOATS
+    if _TORCH is None:
+        import torch
+        _INT32, _FLOAT32 = torch.int32, torch.float32
+        _CODES = {torch.float8_e4m3fn: fa.FA_E4M3, torch.int8: fa.FA_INT8}
+        _FLOATS = {torch.bfloat16: fa.FA_BF16, torch.float16: fa.FA_FP16, torch.float32: fa.FA_FP32}
+        _TORCH = torch
+    return _TORCH
 
 
 def _types():
-    """{code dtype: its number}, {16-bit or output dtype: its number} (torch is imported on first use)."""
-    global _CODES, _FLOATS
-    if _CODES is None:
-        import torch
-        _CODES = {torch.float8_e4m3fn: fa.FA_E4M3, torch.int8: fa.FA_INT8}
-        _FLOATS = {torch.bfloat16: fa.FA_BF16, torch.float16: fa.FA_FP16, torch.float32: fa.FA_FP32}
+    """{code dtype: its number}, {16-bit or output dtype: its number}."""
+    _torch()
     return _CODES, _FLOATS
 
 
@@ -65,11 +71,11 @@ def enter(device, stream):
     """(context, raw stream) of a helper's call on tensors of this device: the context makes their device and
     the caller's stream current, so that what the helper allocates belongs to the stream its kernels run on;
     it is None where both already are."""
-    import torch
+    if stream is None and device.type == "cuda" and device.index == _torch().cuda.current_device():
+        return None, _TORCH._C._cuda_getCurrentRawStream(device.index)
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    if stream is None and device.index == torch.cuda.current_device():
-        return None, torch._C._cuda_getCurrentRawStream(device.index)
+    torch = _TORCH
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -102,26 +108,27 @@ def check_tensor(name, t, dtype, shape, device):
 
 def _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, device):
     """(num_pages, Hkv, page_size, pages_per_seq, code type) of a cache; ValueError unless its tensors fit together."""
-    import torch
-    code = _types()[0].get(k_pages.dtype)
-    shape = k_pages.shape
+    _torch()
+    dtype, shape, table = k_pages.dtype, k_pages.shape, block_table.shape
+    code = _CODES.get(dtype)
     if code is None or len(shape) != 4:
         raise ValueError("k_pages: expected [num_pages, Hkv, page_size, D] of torch.float8_e4m3fn or torch.int8")
     num_pages, heads, page_size, dim = shape
     if (Hkv is not None and heads != Hkv) or dim != D:
         raise ValueError(f"k_pages {list(shape)} does not hold the given heads or head dimension")
-    scales = (num_pages, heads, page_size // 16)
-    check_tensor("k_pages", k_pages, k_pages.dtype, shape, device)
-    check_tensor("v_pages", v_pages, k_pages.dtype, shape, device)
-    check_tensor("k_scales", k_scales, torch.float32, scales, device)
-    check_tensor("v_scales", v_scales, torch.float32, scales, device)
-    if block_table.dim() != 2:
+    if len(table) != 2:
         raise ValueError("block_table: expected [B, pages_per_seq]")
-    pages_per_seq = block_table.shape[1]
-    check_tensor("block_table", block_table, torch.int32, (B, pages_per_seq), device)
-    if seqlens_k is not None:
-        check_tensor("seqlens_k", seqlens_k, torch.int32, (B,), device)
-    return num_pages, heads, page_size, pages_per_seq, code
+    scales = (num_pages, heads, page_size // 16)
+    if not (alike(k_pages, dtype, shape, device) and alike(v_pages, dtype, shape, device) and alike(k_scales, _FLOAT32, scales, device)
+            and alike(v_scales, _FLOAT32, scales, device) and alike(block_table, _INT32, table, device) and table[0] == B
+            and (seqlens_k is None or alike(seqlens_k, _INT32, (B,), device))):
+        check_tensor("k_pages", k_pages, dtype, shape, device)
+        check_tensor("v_pages", v_pages, dtype, shape, device)
+        check_tensor("k_scales", k_scales, _FLOAT32, scales, device)
+        check_tensor("v_scales", v_scales, _FLOAT32, scales, device)
+        check_tensor("block_table", block_table, _INT32, (B, table[1]), device)
+        check_tensor("seqlens_k", seqlens_k, _INT32, (B,), device)
+    return num_pages, heads, page_size, table[1], code
 
 
 def new_kv8_cache(num_pages, page_size, Hkv, D, dtype=None, device="cuda"):
@@ -142,24 +149,24 @@ def append_kv8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_
     ``seqlens_k`` int32 [B]: the lengths with the new rows included; the first ``new_lens[b]`` (int32 [B]; None: all
     Nt) rows of item b become its last keys.  Rows in a strided k or v are copied together first.
     """
-    import torch
-    B, Nt, Hkv, D = k.shape
-    dev = k.device
+    B, Nt, Hkv, D = shape = k.shape
+    dev, dtype = k.device, k.dtype
     num_pages, _, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, dev)
     if new_lens is not None:
-        check_tensor("new_lens", new_lens, torch.int32, (B,), dev)
-    if v.dtype is not k.dtype or v.shape != k.shape or v.device != dev:
+        check_tensor("new_lens", new_lens, _INT32, (B,), dev)
+    if v.dtype is not dtype or v.shape != shape or v.device != dev:
         raise ValueError("k and v must be alike")
     context, raw = enter(dev, stream)
-
-    def call():
-        rk, rv = (k, v) if k.is_contiguous() and v.is_contiguous() else (k.contiguous(), v.contiguous())
-        return (_lib._lib or load()).fa_kv8_append(
-            rk.data_ptr(), rv.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+    if context is not None or not (k.is_contiguous() and v.is_contiguous()):
+        with context or contextlib.nullcontext():
+            k, v = k.contiguous(), v.contiguous()
+            st = fa_kv8_append(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, new_lens, B, Nt, Hkv, num_pages,
+                               page_size, pps, D, raw)
+    else:
+        st = (_lib._lib or load()).fa_kv8_append(
+            k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             block_table.data_ptr(), seqlens_k.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, Nt, Hkv, num_pages,
-            page_size, pps, D, raw, _types()[1].get(k.dtype, -1), code)
-
-    st = in_context(context, call)
+            page_size, pps, D, raw, _FLOATS.get(dtype, -1), code)
     if st != fa.FA_OK:
         raise fa.FAError(st, "fa_kv8_append")
 
@@ -176,28 +183,29 @@ def attend_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k=N
     ``block_table`` int32 [B, pages_per_seq]; ``seqlens_k`` int32 [B] (keys of each sequence, those of the Nq tokens
     included) or None (every table entry in use).  Query i of item b sees keys up to seqlens_k[b] - Nq + i.
     """
-    import torch
     B, Nq, Hq, D = q.shape
-    dev = q.device
+    dev, dtype = q.device, q.dtype
     num_pages, Hkv, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, None, D, dev)
-    floats = _types()[1]
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace: expected a contiguous tensor on the device of q")
     context, raw = enter(dev, stream)
 
     def call():
         rq = q if q.is_contiguous() else q.contiguous()
-        ws = torch.empty(_workspace_bytes(B, Nq, Hq, Hkv, D), device=dev, dtype=torch.uint8) if workspace is None else workspace
-        o = torch.empty_like(rq, dtype=out_dtype)
-        lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
-        st = (_lib._lib or load()).fa_kv8_attend(
+        if workspace is None:
+            size = _workspace_bytes(B, Nq, Hq, Hkv, D)
+            ws = rq.new_empty(size, dtype=_TORCH.uint8)
+        else:
+            ws, size = workspace, workspace.nbytes
+        o = _TORCH.empty_like(rq) if out_dtype is None else _TORCH.empty_like(rq, dtype=out_dtype)
+        lse = rq.new_empty((B, Hq, Nq), dtype=_FLOAT32)
+        return (_lib._lib or load()).fa_kv8_attend(
             rq.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(),
-            o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, num_pages, page_size, pps, D, 1.0 / math.sqrt(D) if scale is None else scale,
-            None if seqlens_k is None else seqlens_k.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), raw,
-            floats.get(q.dtype, -1), code, floats.get(o.dtype, -1))
-        return st, o, lse
+            o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, num_pages, page_size, pps, D, D ** -0.5 if scale is None else scale,
+            None if seqlens_k is None else seqlens_k.data_ptr(), ws.data_ptr(), size, raw, _FLOATS.get(dtype, -1), code,
+            _FLOATS.get(o.dtype, -1)), o, lse
 
-    st, o, lse = in_context(context, call)
+    st, o, lse = call() if context is None else in_context(context, call)
     if st != fa.FA_OK:
         raise fa.FAError(st, "fa_kv8_attend")
     return o, lse

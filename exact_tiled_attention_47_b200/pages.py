@@ -13,9 +13,9 @@ import functools
 
 import exact_tiled_attention_47_b200 as fa
 
-from . import _lib
+from . import _lib, kv8
 from ._lib import load
-from .kv8 import check_tensor, enter, in_context
+from .kv8 import alike, check_tensor, enter, in_context
 
 
 def _pointers(pools):
@@ -83,21 +83,19 @@ def fa_pages_copy(src_pools, dst_pools, page_bytes, src, dst, n, src_num_pages, 
 
 
 def _check_state(block_table, seqlens, refcount):
-    import torch
-    if block_table.dim() != 2 or refcount.dim() != 1:
+    shape, count, dev = block_table.shape, refcount.shape, block_table.device
+    if len(shape) != 2 or len(count) != 1:
         raise ValueError("expected block_table [S, pages_per_seq] and refcount [num_pages]")
-    S, pages_per_seq = shape = block_table.shape
-    dev = block_table.device
-    num_pages = refcount.shape[0]
-    check_tensor("block_table", block_table, torch.int32, shape, dev)
-    check_tensor("seqlens", seqlens, torch.int32, (S,), dev)
-    check_tensor("refcount", refcount, torch.int32, (num_pages,), dev)
-    return S, pages_per_seq, num_pages, dev
+    int32 = kv8._torch().int32
+    if not (alike(block_table, int32, shape, dev) and alike(seqlens, int32, shape[:1], dev) and alike(refcount, int32, count, dev)):
+        check_tensor("block_table", block_table, int32, shape, dev)
+        check_tensor("seqlens", seqlens, int32, shape[:1], dev)
+        check_tensor("refcount", refcount, int32, count, dev)
+    return shape[0], shape[1], count[0], dev
 
 
 def _check_list(name, t, n, dev):
-    import torch
-    check_tensor(name, t, torch.int32, (t.numel() if n is None else n,), dev)
+    check_tensor(name, t, kv8._torch().int32, (t.numel() if n is None else n,), dev)
     return t.numel()
 
 
@@ -123,10 +121,9 @@ def _check_workspace(workspace, dev):
 
 def _workspace(workspace, n, S, num_pages, dev):
     """(tensor, bytes), allocated on the current stream where the caller gave none."""
-    import torch
     if workspace is None:
         need = _workspace_bytes(n, S, num_pages)
-        return torch.empty(need, device=dev, dtype=torch.uint8), need
+        return kv8._TORCH.empty(need, device=dev, dtype=kv8._TORCH.uint8), need
     return workspace, workspace.nbytes
 
 
@@ -196,15 +193,15 @@ def compact_pages(block_table, seqlens, refcount, page_size, pools, in_place=Fal
     ``in_place``: the given block_table and refcount are updated and returned; else new tensors are.  ``remap`` int32
     [num_pages]: the new place of each live page, -1 for free ones; ``n_live`` int32 [1].
     """
-    import torch
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     sizes = _page_bytes(pools, num_pages, dev)
     _check_workspace(workspace, dev)
     context, raw = enter(dev, stream)
 
     def call():
-        table_out, ref_out = (block_table, refcount) if in_place else (torch.empty_like(block_table), torch.empty_like(refcount))
-        remap, n_live = torch.empty_like(refcount), torch.empty(1, device=dev, dtype=torch.int32)
+        like = kv8._TORCH.empty_like
+        table_out, ref_out = (block_table, refcount) if in_place else (like(block_table), like(refcount))
+        remap, n_live = like(refcount), refcount.new_empty(1)
         ws, size = _workspace(workspace, 1, S, num_pages, dev)
         st = (_lib._lib or load()).fa_pages_compact(
             block_table.data_ptr(), seqlens.data_ptr(), refcount.data_ptr(), table_out.data_ptr(), ref_out.data_ptr(), remap.data_ptr(),
