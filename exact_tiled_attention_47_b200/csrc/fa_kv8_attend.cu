@@ -42,6 +42,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGranule = 64;  // keys: one block of 16 for each warp
+constexpr int kUnitCost = 4;  // granules that a unit's fixed cost stands for (2 and 8: 102 and 96 us where 4 takes 94, B64 ragged 8192)
+constexpr int kMinShare = 8;
 constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (64 rows: 76 us here and 95 there,
                                // 128 rows: 75 and 65; B8, 8 KV heads, D 128, 4096 and 2048 keys)
 
@@ -139,7 +141,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 
 template <bool kFp16, bool kInt8, int D, int NG>
-__global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const AttParams p, const int o_fp32) {
+__global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const __grid_constant__ AttParams p, const int o_fp32) {
   using R = Ring<D, NG>;
   constexpr int kRows = R::kRows, kStages = R::kStages;
   constexpr int LD = D / 64;  // 16-byte pieces of a K row per lane
@@ -153,9 +155,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
   const long long outs = static_cast<long long>(p.B) * p.Nq * p.Hq;
   const long long pool = (static_cast<long long>(p.num_pages) * p.Hkv) << p.page_shift;
 
-  write_tiles_without_keys<kFp16, D, kRows>(p, o_fp32);
   asm volatile("griddepcontrol.launch_dependents;");
   const Place place = find_place<kRows, kThreads>(p, gridDim.x, blockIdx.x, scan);
+  if (place.short_items) write_tiles_without_keys<kFp16, D, kRows>(p, o_fp32);
   if (place.b < 0) return;
   Walk walk = walk_of(p, place, gridDim.x, blockIdx.x);
 
@@ -504,9 +506,10 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
   p.granule = cap <= kShortKeys ? kShortKeys : kGranule;
   p.over = p.granule == kGranule ? kUnitCost : 0;
+  p.least = p.over ? kMinShare : 1;
   // no more CTAs than the fullest tables could give work to
   const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
-  const int grid = static_cast<int>(std::min<long long>(kCtas, p.over ? (most + kMinShare - 1) / kMinShare : most));
+  const int grid = static_cast<int>(std::min<long long>(kCtas, (most + p.least - 1) / p.least));
   kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
   if (p.over && grid > 1)
     if (const int e = launch_combine8<kFp16, D, R::kRows>(p, a.o_fp32, grid, stream)) return e;

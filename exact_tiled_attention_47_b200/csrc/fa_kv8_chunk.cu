@@ -17,8 +17,8 @@
 //   - the grid is one CTA per SM and shares the work evenly (fa_kv8_sched.cuh), pieces of cut units are
 //     merged by a second kernel.
 // Tensor memory: S0 S1 [0, 256), O0 O1 [256, 256 + 2 D).  Warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: MMA
-// issue (10 and 11 idle); 12-15: conversion.  16 warps leave the softmax 168 registers a thread, so a row of S is never
-// held as a whole: its two halves are read for the maxima, the second is turned into weights, the first is read again.
+// issue (10 and 11 idle); 12-15: conversion.  16 warps share the registers, so a row of S is never held as a whole: its
+// two halves are read for the maxima, the second is turned into weights and stored, the first is read again.
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -38,14 +38,16 @@ constexpr int kMmaWarp = 8;       // owns TMEM; issues the MMAs of tile 0 (warp 
 constexpr int kConvWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPanelBytes = kBM * 128;  // 64 fp16 columns of a tile
-constexpr int kChunkUnitCost = 3;       // blocks that the fixed cost of a unit stands for
-// Registers: launched with kLaunchRegs per thread; the MMA and conversion warpgroups give some to the two of the softmax.  The
-// sum must not exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms the
-// launch allocation once per device.
+constexpr int kChunkUnitCost = 2;       // blocks that the fixed cost of a unit stands for
+constexpr int kChunkMinShare = 4;       // (Nq 244, 1 head of each group, 1248 keys, B3: 43 us, with 8 53)
+// Registers: launched with kLaunchRegs per thread; the MMA warpgroup gives some to the others.  The sum must not
+// exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms that allocation once per
+// device.  (Of the splits that leave little in local memory this one was the fastest: chunk of 1024 behind 16384
+// keys 717 us, with 160 / 56 / 136 727, with 168 / 56 / 120 737.)
 constexpr int kLaunchRegs = 128;
-constexpr int kSoftmaxRegs = 168;
-constexpr int kControlRegs = 56;
-constexpr int kConvRegs = 120;
+constexpr int kSoftmaxRegs = 144;
+constexpr int kControlRegs = 80;
+constexpr int kConvRegs = 144;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kConvRegs <= 4 * kLaunchRegs, "register split");
 
 template <int D>
@@ -184,9 +186,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.Nq * p.group;
 
-  write_tiles_without_keys<kFp16, D, kUnitRows>(p, o_fp32);
   asm volatile("griddepcontrol.launch_dependents;");
   const Place place = find_place<kUnitRows, kChunkThreads>(p, gridDim.x, blockIdx.x, bars->scan);
+  if (place.short_items) write_tiles_without_keys<kFp16, D, kUnitRows>(p, o_fp32);
   if (place.b < 0) return;  // uniform
   __syncthreads();  // scan and what lies in its place may be written
   if (threadIdx.x < 4) bars->walk[threadIdx.x] = walk_of(p, place, gridDim.x, blockIdx.x);
@@ -225,7 +227,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
   int n0 = 0;  // key blocks of the pieces before this one
 
   if (warp >= kConvWarp) {
-    regs_decrease<kConvRegs>();
+    if constexpr (kConvRegs > kLaunchRegs) regs_increase<kConvRegs>();
+    else if constexpr (kConvRegs < kLaunchRegs) regs_decrease<kConvRegs>();
     // ================================ conversion =================================================
     const int cw = warp - kConvWarp;
     const int r8 = lane >> 2, c4 = lane & 3;  // row of a group of eight, 16-code chunk of a 64-column panel
@@ -539,28 +542,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
           }
         }
         uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
-        uint32_t pk[4][16];
         const bool own = __any_sync(0xffffffffu, mo - m > lv_min + 64.f);
+        uint32_t pk[2][16];
         auto weigh = [&](int half) {
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             const uint32_t sc = scale + (half * 4 + ch * 2) * 8;
-            uint32_t(&out)[16] = pk[half * 2 + ch];
-            if (own) weights32<true>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
-            else weights32<false>(sr, ch, sc, qs, m, mo, acc0, acc1, out);
+            if (own) weights32<true>(sr, ch, sc, qs, m, mo, acc0, acc1, pk[ch]);
+            else weights32<false>(sr, ch, sc, qs, m, mo, acc0, acc1, pk[ch]);
           }
         };
+        auto put = [&](int half) {
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sts128(tile_at(pbase, r, half * 8 + ch * 4 + q), pk[ch][4 * q], pk[ch][4 * q + 1], pk[ch][4 * q + 2], pk[ch][4 * q + 3]);
+        };
         weigh(1);
-        read(0);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->s_free[t]);
-        weigh(0);
-        lsum = f2_add(lsum, f2_add(acc0, acc1));
-        if (j > 0) {
+        if (j > 0) {  // P and O belong to the product before until it is done
           if (!(ok = warp_wait(&bars->o_done[t], (c0 + j - 1) & 1, abort_flag, p.status))) break;
           tc_fence_after();
         }
+        put(1);
         if (rescale) {
 #pragma unroll
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -571,11 +575,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
             tmem_st32(lane_base + C::col_o(t) + ch * 32, orr);
           }
         }
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            sts128(tile_at(pbase, r, ch * 4 + q), pk[ch][4 * q], pk[ch][4 * q + 1], pk[ch][4 * q + 2], pk[ch][4 * q + 3]);
+        read(0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[t]);
+        weigh(0);
+        put(0);
+        lsum = f2_add(lsum, f2_add(acc0, acc1));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (rescale) tmem_wait_st();
         tc_fence_before();
@@ -649,8 +655,9 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
   p.granule = cap <= kShortKeys ? kShortKeys : kBN;
   p.over = p.granule == kBN ? kChunkUnitCost : 0;
+  p.least = p.over ? kChunkMinShare : 1;
   const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
-  const int grid = static_cast<int>(std::min<long long>(kSms, p.over ? (most + kMinShare - 1) / kMinShare : most));
+  const int grid = static_cast<int>(std::min<long long>(kSms, (most + p.least - 1) / p.least));
   kern<<<grid, kChunkThreads, ChunkCfg<D>::kSmemBytes, stream>>>(p, a.o_fp32);
   if (p.over && grid > 1)
     if (const int e = launch_combine8<kFp16, D, kUnitRows>(p, a.o_fp32, grid, stream)) return e;

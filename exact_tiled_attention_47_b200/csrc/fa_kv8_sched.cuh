@@ -13,8 +13,6 @@ constexpr int kSms = 148;
 constexpr float kLazy = 8.f;     // log2 units by which a maximum may be exceeded before it is raised
 constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that differences with -inf are defined)
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
-constexpr int kMinShare = 8;      // granules (a unit's fixed cost included) of a share: shorter ones cost more to merge than to read
-constexpr int kUnitCost = 4;      // granules that the fixed cost of a unit (queries, filling the ring, merging the warps) stands for
 constexpr int kShortKeys = 512;   // tables up to this many keys: a granule is a whole unit, and nothing is merged
 
 
@@ -32,7 +30,9 @@ struct AttParams {
   float* ws_l;  // [2 * shares, rows of a tile]
   int B, Nq, Hq, Hkv, group, tiles;
   int granule;  // keys
-  int over;     // kUnitCost, or 0 where a granule is a whole unit
+  int over;     // granules that the fixed cost of a unit (queries, the first tiles, the merge) stands for; 0: a
+                // granule is a whole unit, and no unit is cut
+  int least;    // cost of the smallest share: shorter ones cost more to merge than to read
   int num_pages, page_shift, pps;
   float scale_log2;
   int* status;
@@ -107,6 +107,7 @@ struct Place {
   long long total;  // cost of all items
   long long off;
   int b;
+  bool short_items;  // some item has fewer keys than queries (or a length out of range)
 };
 
 template <int kThreads>
@@ -118,8 +119,7 @@ struct ScanMem {
 
 // Number of shares of a total cost, and where share c begins.
 __device__ __forceinline__ int shares_of(const AttParams& p, long long total, int grid) {
-  const int least = p.over ? kMinShare : 1;
-  return static_cast<int>(min(static_cast<long long>(grid), (total + least - 1) / least));
+  return static_cast<int>(min(static_cast<long long>(grid), (total + p.least - 1) / p.least));
 }
 __device__ __forceinline__ long long share_begin(long long total, int shares, int c) {
   if (total < (1LL << 31)) {  // (a 64-bit division takes a hundred instructions)
@@ -137,11 +137,16 @@ __device__ __forceinline__ Place find_place(const AttParams& p, int grid, int c,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place r;
   long long mine = 0, sum = 0;
-  for (int b = tid; b < p.B; b += kThreads) sum += (mine = item_cost<kRows>(p, keys_of(p, b)));
+  bool few = false;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int len = keys_of(p, b);
+    few |= len < p.Nq;
+    sum += (mine = item_cost<kRows>(p, len));
+  }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sm.sums[warp] = sum;
-  __syncthreads();
+  r.short_items = __syncthreads_or(few) != 0;
   r.total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) r.total += sm.sums[w];
@@ -267,26 +272,30 @@ __device__ __forceinline__ bool next_piece(const AttParams& p, Walk& w, Piece& s
   return false;
 }
 
-// O = 0 and LSE = -inf for the rows of tiles that see no key, and the report of lengths out of range; the
-// items are spread over the grid.
+// O = 0 and LSE = -inf for the rows of tiles that see no key (only items with fewer keys than queries have any), and
+// the report of lengths out of range; every item's rows are spread over the grid.
 template <bool kFp16, int D, int kRows>
 __device__ __forceinline__ void write_tiles_without_keys(const AttParams& p, int o_fp32) {
-  const int rows = p.Nq * p.group, tid = threadIdx.x, threads = blockDim.x;
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (p.seqlens && tid == 0) {
-      const int len = __ldg(p.seqlens + b);
-      if (len < 0 || len > (p.pps << p.page_shift)) record_status(p.status, kStatusCuSeqlens);
-    }
+  const int rows = p.Nq * p.group;
+  for (int b = 0; b < p.B; ++b) {
     const int len = keys_of(p, b);
-    for (int tile = 0; tile < p.tiles && tile_keys<kRows>(p, len, tile) == 0; ++tile) {
-      const long long n = static_cast<long long>(min(rows - tile * kRows, kRows)) * p.Hkv * (D / 2);
-      for (long long i = tid; i < n; i += threads) {
-        const int r = static_cast<int>(i / (D / 2)), row = tile * kRows + r / p.Hkv, hk = r % p.Hkv, d = static_cast<int>(i % (D / 2)) * 2;
-        const size_t at = o_row(p, b, hk, row);
-        if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
-        store2<kFp16>(p.o, at * D + d, 0.f, 0.f, o_fp32 != 0);
-        if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
-      }
+    if (len >= p.Nq) continue;
+    if (p.seqlens && blockIdx.x == 0 && threadIdx.x == 0) {
+      const int given = __ldg(p.seqlens + b);
+      if (given < 0 || given > (p.pps << p.page_shift)) record_status(p.status, kStatusCuSeqlens);
+    }
+    // rows of the first Nq - len tokens see no key; the tiles that hold nothing else
+    const long long none = static_cast<long long>(p.Nq - len) * p.group;
+    const int dead = none >= rows ? rows : static_cast<int>(none / kRows * kRows);
+    const long long n = static_cast<long long>(dead) * p.Hkv * (D / 8);
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * blockDim.x) {
+      const unsigned r = static_cast<unsigned>(i / (D / 8));
+      const int row = static_cast<int>(r / static_cast<unsigned>(p.Hkv)), hk = static_cast<int>(r % static_cast<unsigned>(p.Hkv)), d = static_cast<int>(i % (D / 8)) * 8;
+      const size_t at = o_row(p, b, hk, row);
+      if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) store2<kFp16>(p.o, at * D + d + e, 0.f, 0.f, o_fp32 != 0);
+      if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
     }
   }
 }
@@ -294,10 +303,11 @@ __device__ __forceinline__ void write_tiles_without_keys(const AttParams& p, int
 // Merges the pieces of the units that lie in more than one share.  CTA i looks at the border between
 // shares i and i + 1 and takes the unit it cuts, if no earlier border cuts the same one: piece 0 is the
 // end of share i, the others are the beginnings of shares i + 1, i + 2, ...  O = sum_s exp(lse_s - M) o_s /
-// sum_s exp(lse_s - M), LSE = M + ln of that sum; a warp holds its rows side by side, 32 rows of a tile to a CTA.
+// sum_s exp(lse_s - M), LSE = M + ln of that sum; two rows to a warp, eight of a tile to a CTA (long
+// contexts of few heads come in a hundred pieces: one after another they took 100 us).
 constexpr int kCombineThreads = 128;
 template <int kRows>
-constexpr int kCombineRows = kRows < 32 ? kRows : 32;
+constexpr int kCombineRows = 8;
 
 template <bool kFp16, int D, int kRows>
 __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttParams p, const int o_fp32, const int grid) {
@@ -322,32 +332,44 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
   float M[RPW], sum[RPW], acc[RPW][PER];
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
+    const int row = part + warp + i * kWarps;
     M[i] = kNone;
+    for (int s = lane; s <= pieces && row < rows; s += 32) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], o));
     sum[i] = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
   }
-  for (int s = 0; s <= pieces; ++s)
+  // eight pieces' loads are under way at once
+  for (int s0 = 0; s0 <= pieces; s0 += 8) {
+    float w[RPW][8];
+    float2 x[RPW][8][PER / 2];
 #pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int row = part + warp + i * kWarps;
-      if (row < rows) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
-    }
-  for (int s = 0; s <= pieces; ++s)
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int row = part + warp + i * kWarps;
-      if (row >= rows) continue;
-      const float w = ex2(p.ws_l[slot(s) + row] * kLog2e - M[i]);
-      sum[i] += w;
-      const float2* x = reinterpret_cast<const float2*>(p.ws_o + (slot(s) + row) * D) + lane * (PER / 2);
+      for (int i = 0; i < RPW; ++i) {
+        const int row = part + warp + i * kWarps;
+        const bool in = s0 + k <= pieces && row < rows;
+        const size_t at = slot(in ? s0 + k : 0) + (in ? row : 0);
+        w[i][k] = in ? p.ws_l[at] : -INFINITY;
+        const float2* src = reinterpret_cast<const float2*>(p.ws_o + at * D) + lane * (PER / 2);
 #pragma unroll
-      for (int e = 0; e < PER / 2; ++e) {
-        const float2 y = x[e];
-        acc[i][2 * e] = fmaf(w, y.x, acc[i][2 * e]);
-        acc[i][2 * e + 1] = fmaf(w, y.y, acc[i][2 * e + 1]);
+        for (int e = 0; e < PER / 2; ++e) x[i][k][e] = in ? src[e] : make_float2(0.f, 0.f);
       }
-    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < RPW; ++i) {
+        const float f = ex2(w[i][k] * kLog2e - M[i]);
+        sum[i] += f;
+#pragma unroll
+        for (int e = 0; e < PER / 2; ++e) {
+          acc[i][2 * e] = fmaf(f, x[i][k][e].x, acc[i][2 * e]);
+          acc[i][2 * e + 1] = fmaf(f, x[i][k][e].y, acc[i][2 * e + 1]);
+        }
+      }
+  }
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
     const int row = part + warp + i * kWarps, rr = u.tile * kRows + row;
