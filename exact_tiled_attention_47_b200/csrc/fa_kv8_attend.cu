@@ -44,6 +44,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGranule = 64;  // keys: one block of 16 for each warp
 constexpr int kUnitCost = 4;  // granules that a unit's fixed cost stands for (2 and 8: 102 and 96 us where 4 takes 94, B64 ragged 8192)
 constexpr int kMinShare = 8;
+constexpr int kWholeKeys = 1024;  // tables up to this many keys: a granule is a whole unit, nothing is merged
 constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (64 rows: 76 us here and 95 there,
                                // 128 rows: 75 and 65; B8, 8 KV heads, D 128, 4096 and 2048 keys)
 
@@ -504,7 +505,7 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   p.ws_o = static_cast<float*>(a.ws);
   p.ws_l = p.ws_o + static_cast<size_t>(2) * kCtas * R::kRows * D;
   const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
-  p.granule = cap <= kShortKeys ? kShortKeys : kGranule;
+  p.granule = cap <= kWholeKeys ? kWholeKeys : kGranule;
   p.over = p.granule == kGranule ? kUnitCost : 0;
   p.least = p.over ? kMinShare : 1;
   // no more CTAs than the fullest tables could give work to

@@ -39,6 +39,7 @@ constexpr int kConvWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kPanelBytes = kBM * 128;  // 64 fp16 columns of a tile
 constexpr int kChunkUnitCost = 2;       // blocks that the fixed cost of a unit stands for
+constexpr int kChunkWholeKeys = 512;    // tables up to this many keys: a granule is a whole unit, nothing is merged
 constexpr int kChunkMinShare = 4;       // (Nq 244, 1 head of each group, 1248 keys, B3: 43 us, with 8 53)
 // Registers: launched with kLaunchRegs per thread; the MMA warpgroup gives some to the others.  The sum must not
 // exceed the launch allocation, else setmaxnreg.inc would wait forever; the host confirms that allocation once per
@@ -653,7 +654,7 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   p.ws_o = static_cast<float*>(a.ws);
   p.ws_l = p.ws_o + static_cast<size_t>(2) * kSms * kUnitRows * D;
   const long long cap = static_cast<long long>(a.c.pages_per_seq) * a.c.page_size;
-  p.granule = cap <= kShortKeys ? kShortKeys : kBN;
+  p.granule = cap <= kChunkWholeKeys ? kChunkWholeKeys : kBN;
   p.over = p.granule == kBN ? kChunkUnitCost : 0;
   p.least = p.over ? kChunkMinShare : 1;
   const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;

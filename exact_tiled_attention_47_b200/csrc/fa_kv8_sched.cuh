@@ -13,7 +13,6 @@ constexpr int kSms = 148;
 constexpr float kLazy = 8.f;     // log2 units by which a maximum may be exceeded before it is raised
 constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that differences with -inf are defined)
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
-constexpr int kShortKeys = 512;   // tables up to this many keys: a granule is a whole unit, and nothing is merged
 
 
 struct AttParams {

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const PlanParams p
 }
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PlanParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int cnt[kPlanPer * 32], sums[32], s_bad;
   const int tid = threadIdx.x;
   int bad = 0, total = 0;
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PlanParam
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PlanParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int cnt[kPlanPer * 32], sums[32];
   int live = 0;
   for (int page = threadIdx.x; page < p.num_pages; page += kPlanThreads) live += p.refs[page] > 0;
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PlanPa
 // Checks a list of page copies: indices inside the pools, no destination twice, and no page that is
 // both read and written (pools may be the same on both sides).
 __global__ void __launch_bounds__(kPlanThreads) copy_plan_kernel(const PlanParams p, bool same) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int s_bad;
   int bad = 0;
   if (threadIdx.x == 0) p.w.head[0] = p.w.head[1] = 0;
@@ -394,11 +397,15 @@ __device__ __forceinline__ void move_pages(const MoveParams& m, int block, int b
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ MoveParams m) { move_pages(m, blockIdx.x, gridDim.x); }
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ MoveParams m) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
+  move_pages(m, blockIdx.x, gridDim.x);
+}
 
 // Fork: the first p.n CTAs write the destinations' table rows and count the shared pages, the others
 // copy the last partial pages.
 __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constant__ MoveParams m, const PlanParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
   if (m.head[1] == 0) return;
   if (static_cast<int>(blockIdx.x) >= p.n) {
     move_pages(m, blockIdx.x - p.n, gridDim.x - p.n);
@@ -418,6 +425,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
 // Tables and counts may be written in place: each entry is read and written by one thread alone.
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ MoveParams m, const PlanParams p, int* table_out,
                                                                int* refs_out, int meta) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
   if (static_cast<int>(blockIdx.x) >= meta) {
     move_pages(m, blockIdx.x - meta, gridDim.x - meta);
     return;
@@ -437,15 +445,33 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
     table_out[i] = page;
   }
   for (long long j = first; j < movers; j += step) refs_out[m.pdst[j]] = p.refs[m.psrc[j]];
-  for (long long i = first; i < p.num_pages; i += step) {
-    // places of moved pages are written by the loop above (from counts that lie behind n_live) and
-    // those behind n_live are cleared by the kernel that follows
-    if (i < n_live && p.refs[i] > 0) refs_out[i] = p.refs[i];
+  // places of moved pages are written above; in place, those behind n_live are still read there, and a kernel that
+  // follows clears them
+  for (long long i = first; refs_out != p.refs && i < p.num_pages; i += step) {
+    const int r = p.refs[i];
+    if (i >= n_live) refs_out[i] = 0;
+    else if (r > 0) refs_out[i] = r;
   }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) clear_tail_kernel(const int* n_live, int* refs_out, int num_pages) {
   for (int i = *n_live + static_cast<int>(blockIdx.x) * kMoveThreads + threadIdx.x; i < num_pages; i += gridDim.x * kMoveThreads) refs_out[i] = 0;
+}
+
+// The work's kernel is launched while the plan still runs and waits for it on the device (the gap between the two
+// is a good part of a small request's time).
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kern)(P...), int grid, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 PlanParams plan_of(const PagesArgs& a) {
@@ -516,8 +542,8 @@ int launch_pages_fork(const PagesArgs& a, cudaStream_t stream) {
   fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   for (int first = 0; first == 0 || first < a.n_pools; first += kMaxPools) {
     const MoveParams m = move_of(a, p, first);
-    if (first == 0) fork_kernel<<<a.n + move_blocks(m, a.n), kMoveThreads, 0, stream>>>(m, p);
-    else move_kernel<<<move_blocks(m, a.n), kMoveThreads, 0, stream>>>(m);
+    const cudaError_t e = first == 0 ? launch_behind(fork_kernel, a.n + move_blocks(m, a.n), stream, m, p) : launch_behind(move_kernel, move_blocks(m, a.n), stream, m);
+    if (e != cudaSuccess) return static_cast<int>(e);
   }
   return static_cast<int>(cudaGetLastError());
 }
@@ -528,10 +554,11 @@ int launch_pages_compact(const PagesArgs& a, cudaStream_t stream) {
   const int meta = static_cast<int>(std::min<long long>(148, (static_cast<long long>(a.S) * a.pages_per_seq + a.num_pages) / 1024 + 1));
   for (int first = 0; first == 0 || first < a.n_pools; first += kMaxPools) {
     const MoveParams m = move_of(a, p, first);
-    if (first == 0) compact_kernel<<<meta + move_blocks(m, a.num_pages), kMoveThreads, 0, stream>>>(m, p, a.table_out, a.refs_out, meta);
-    else move_kernel<<<move_blocks(m, a.num_pages), kMoveThreads, 0, stream>>>(m);
+    const cudaError_t e = first == 0 ? launch_behind(compact_kernel, meta + move_blocks(m, a.num_pages), stream, m, p, a.table_out, a.refs_out, meta)
+                                     : launch_behind(move_kernel, move_blocks(m, a.num_pages), stream, m);
+    if (e != cudaSuccess) return static_cast<int>(e);
   }
-  clear_tail_kernel<<<std::min(148, a.num_pages / 1024 + 1), kMoveThreads, 0, stream>>>(a.n_live, a.refs_out, a.num_pages);
+  if (a.refs_out == a.refs) clear_tail_kernel<<<std::min(148, a.num_pages / 1024 + 1), kMoveThreads, 0, stream>>>(a.n_live, a.refs_out, a.num_pages);
   return static_cast<int>(cudaGetLastError());
 }
 
@@ -543,7 +570,8 @@ int launch_pages_copy(const PagesArgs& a, cudaStream_t stream) {
   copy_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, same);
   for (int first = 0; first < a.n_pools; first += kMaxPools) {
     const MoveParams m = move_of(a, p, first);
-    move_kernel<<<move_blocks(m, a.n), kMoveThreads, 0, stream>>>(m);
+    const cudaError_t e = launch_behind(move_kernel, move_blocks(m, a.n), stream, m);
+    if (e != cudaSuccess) return static_cast<int>(e);
   }
   return static_cast<int>(cudaGetLastError());
 }
