@@ -79,7 +79,7 @@ __device__ __forceinline__ float2 value2(uint32_t two) {  // two codes in the lo
 }
 
 template <bool kFp16, bool kInt8, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 3) kv8_append_kernel(const AppendParams p) {
   constexpr int LPR = D / 16;        // lanes per row
   constexpr int RPI = 32 / LPR;      // rows per step
   constexpr int IT = kKv8Block / RPI;
