@@ -315,28 +315,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
           if (at >= 0) sc = make_float2(__ldg(p.ks + (at >> 4)), __ldg(p.vs + (at >> 4)));
         }
       };
-      // the queries (before the first codes are loaded: both at once would not fit the registers)
+      // the queries (before the first codes are loaded: both at once would not fit the registers), a tile's 32 rows
+      // of this warp at once
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         if (pc.row0 + t * kBM >= rows) break;
-#pragma unroll 1
+        uint32_t w[4][D / 8];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = cw * 32 + i * 8 + r8, q = pc.row0 + t * kBM + r;
+          const int q = pc.row0 + t * kBM + cw * 32 + i * 8 + r8;
           const bool in = q < rows;
           const size_t at = o_row(p, pc.b, hk, in ? q : pc.row0) * D + c4 * (D / 4);
-          uint32_t w[D / 8];
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             const bool rd = in && idx_ok(p.status, at + 8 * k, 8, static_cast<long long>(p.B) * p.Nq * p.Hq * D);
             const uint4 x = rd ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at) + k) : make_uint4(0, 0, 0, 0);
-            w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+            w[i][4 * k] = x.x; w[i][4 * k + 1] = x.y; w[i][4 * k + 2] = x.z; w[i][4 * k + 3] = x.w;
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = cw * 32 + i * 8 + r8;
           int down = 0;
           if constexpr (!kFp16) {
             float top = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-              const float2 f = unpack2<false>(w[k]);
+              const float2 f = unpack2<false>(w[i][k]);
               top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -346,13 +351,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
             down = e - 14;
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-              const float2 f = unpack2<false>(w[k]);
-              w[k] = pack2<true>(f.x * up, f.y * up);
+              const float2 f = unpack2<false>(w[i][k]);
+              w[i][k] = pack2<true>(f.x * up, f.y * up);
             }
           }
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            sts128(tile_at(sQ + t * C::kTileBytes, r, c4 * (D / 32) + k), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            sts128(tile_at(sQ + t * C::kTileBytes, r, c4 * (D / 32) + k), w[i][4 * k], w[i][4 * k + 1], w[i][4 * k + 2], w[i][4 * k + 3]);
           if (c4 == 0) bars->qexp[s & 1][t * kBM + r] = static_cast<signed char>(down);
         }
       }
@@ -487,8 +492,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         if (lane == 0) mbar_arrive(&bars->q_taken);
         continue;
       }
-      const int lim = row < rows ? min(row_limit(p, pc.len, row), pc.hi) : 0;  // keys below it are visible
-      const int all = tile0 + kBM <= rows ? min(row_limit(p, pc.len, tile0), pc.hi) : 0;  // to every row
+      // keys visible to this row, and to every row of the tile (rows behind the last one are zeros and see all)
+      const int lim = row < rows ? min(row_limit(p, pc.len, row), pc.hi) : pc.hi;
+      const int all = min(row_limit(p, pc.len, tile0), pc.hi);
       float m = kNone, mo = kNone, qs = 0.f;
       uint64_t lsum = f2(0.f, 0.f);
       for (int j = 0; j < blocks; ++j) {

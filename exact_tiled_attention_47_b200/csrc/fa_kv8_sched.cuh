@@ -1,6 +1,8 @@
 // fa_kv8_sched.cuh -- what the two attention kernels of the 8-bit cache share: their parameters, the even
 // division of ragged work over the CTAs, and the kernel that merges units cut by it.
 #pragma once
+#include <algorithm>
+
 #include "fa_internal.h"
 #include "fa_kv8.h"
 #include "fa_prefill_common.cuh"
@@ -391,7 +393,8 @@ int launch_combine8(const AttParams& p, int o_fp32, int grid, cudaStream_t strea
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, kRows / kCombineRows<kRows>);
+  const long long rows = std::min<long long>(kRows, static_cast<long long>(p.Nq) * p.group);  // of the largest tile
+  cfg.gridDim = dim3(grid - 1, static_cast<unsigned>((rows + kCombineRows<kRows> - 1) / kCombineRows<kRows>));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
