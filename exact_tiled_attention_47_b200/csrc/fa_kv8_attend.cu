@@ -125,20 +125,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
-  return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
-  return r;
 }
 
 template <bool kFp16, bool kInt8, int D, int NG>
@@ -162,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
   if (place.b < 0) return;
   Walk walk = walk_of(p, place, gridDim.x, blockIdx.x);
 
-  const uint32_t ring = smem_addr(smem) + warp * R::kWarp, ring_s = ring + kStages * R::kStage;
+  const uint8_t* own_ring = smem + warp * R::kWarp;
+  const uint32_t ring = smem_addr(own_ring), ring_s = ring + kStages * R::kStage;
 
   Piece pc;
   while (next_piece<kRows>(p, walk, pc)) {
@@ -294,16 +284,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       }
       cp_wait<kStages - 1>();
       __syncwarp();
-      const uint32_t kb = ring + st * R::kStage, vb = kb + R::kBlock;
-      float ks, vs;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(ring_s + st * 16) : "memory");
+      const uint8_t *kb = own_ring + st * R::kStage, *vb = kb + R::kBlock;
+      const float2 kvs = *reinterpret_cast<const float2*>(own_ring + kStages * R::kStage + st * 16);
+      const float ks = kvs.x, vs = kvs.y;
       const int key0 = key_w + i * (kWarps * kKv8Block);
 
       // S^T: element e of accumulator n: key g + 8 (e >> 1), row 8 n + 2 t + (e & 1)
       float sc[NG][4] = {};
 #pragma unroll
       for (int c = 0; c < LD; ++c) {
-        const uint4 x = lds128(kb + ring_off<D>(g, t + 4 * c)), y = lds128(kb + ring_off<D>(g + 8, t + 4 * c));
+        const uint4 x = *reinterpret_cast<const uint4*>(kb + ring_off<D>(g, t + 4 * c)), y = *reinterpret_cast<const uint4*>(kb + ring_off<D>(g + 8, t + 4 * c));
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -318,33 +308,38 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       const bool edge = key0 + kKv8Block > min(tile_all, hi);
       const float lv = lg2(fmaxf(vs, 1.17549435e-38f));  // a scale of zero stands for values of zero
       uint32_t wb[NG][2];
+      float f[NG][2], mx[NG][2];
+      bool past = false;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const float f[2] = {qs[n][0] * ks, qs[n][1] * ks};
         if (edge) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (key0 + g + 8 * (e >> 1) >= lim[n][e & 1]) sc[n][e] = -INFINITY;
         }
-        // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks)
-        float mx[2];
-        bool past = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          f[n][e] = qs[n][e] * ks;
           const float top = fmaxf(sc[n][e], sc[n][2 + e]);
-          mx[e] = top == -INFINITY ? -INFINITY : top * f[e];  // (-inf stays what it is where the scale is zero)
-          past |= mx[e] > fminf(m[n][e], mo[n][e] - lv) + kLazy;
+          mx[n][e] = top == -INFINITY ? -INFINITY : top * f[n][e];  // (-inf stays what it is where the scale is zero)
+          past |= mx[n][e] > fminf(m[n][e], mo[n][e] - lv) + kLazy;
         }
-        if (__any_sync(0xffffffffu, past)) {
+      }
+      // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks; one vote for
+      // all rows, so that everything behind it is straight code)
+      if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            float top = mx[n][e];
 #pragma unroll
-            for (int s2 = 4; s2 <= 16; s2 <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], s2));
-            if (mx[e] > m[n][e]) {
-              l[n][e] *= ex2(m[n][e] - mx[e]);
-              m[n][e] = mx[e];
+            for (int s2 = 4; s2 <= 16; s2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s2));
+            if (top > m[n][e]) {
+              l[n][e] *= ex2(m[n][e] - top);
+              m[n][e] = top;
             }
-            const float mv = mx[e] + lv;
+            const float mv = top + lv;
             if (mv > mo[n][e]) {
               const float a = ex2(mo[n][e] - mv);
 #pragma unroll
@@ -355,12 +350,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
               mo[n][e] = mv;
             }
           }
-        }
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
         float p2[4], w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p2[e] = fmaf(sc[n][e], f[e & 1], -m[n][e & 1]);
-          w[e] = fmaf(sc[n][e], f[e & 1], lv - mo[n][e & 1]);
+          p2[e] = fmaf(sc[n][e], f[n][e & 1], -m[n][e & 1]);
+          w[e] = fmaf(sc[n][e], f[n][e & 1], lv - mo[n][e & 1]);
         }
         if (edge) {
 #pragma unroll
@@ -380,10 +377,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       for (int k = 0; k < 4; ++k) {
         const int r = (k >> 1) * 8 + 2 * t + (k & 1);
         if constexpr (D == 128) {
-          const uint4 x = lds128(vb + ring_off<D>(r, g));
+          const uint4 x = *reinterpret_cast<const uint4*>(vb + ring_off<D>(r, g));
           v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
         } else {
-          const uint2 x = lds64(vb + ring_off<D>(r, g >> 1) + (g & 1) * 8);
+          const uint2 x = *reinterpret_cast<const uint2*>(vb + ring_off<D>(r, g >> 1) + (g & 1) * 8);
           v[k][0] = x.x; v[k][1] = x.y;
         }
       }
