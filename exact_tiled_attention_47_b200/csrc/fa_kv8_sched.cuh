@@ -274,29 +274,42 @@ __device__ __forceinline__ bool next_piece(const AttParams& p, Walk& w, Piece& s
 }
 
 // O = 0 and LSE = -inf for the rows of tiles that see no key (only items with fewer keys than queries have any), and
-// the report of lengths out of range; every item's rows are spread over the grid.
+// the report of lengths out of range.  An item with few such rows is left to one CTA, many rows are spread over the
+// grid; a warp looks at 32 items at once.
 template <bool kFp16, int D, int kRows>
 __device__ __forceinline__ void write_tiles_without_keys(const AttParams& p, int o_fp32) {
-  const int rows = p.Nq * p.group;
-  for (int b = 0; b < p.B; ++b) {
-    const int len = keys_of(p, b);
-    if (len >= p.Nq) continue;
-    if (p.seqlens && blockIdx.x == 0 && threadIdx.x == 0) {
-      const int given = __ldg(p.seqlens + b);
+  const int rows = p.Nq * p.group, lane = threadIdx.x & 31;
+  // rows of the first Nq - len tokens see no key; of those, the ones in tiles that hold nothing else
+  auto dead_rows = [&](int len) {
+    const long long none = static_cast<long long>(p.Nq - len) * p.group;
+    return none >= rows ? rows : static_cast<int>(none / kRows * kRows);
+  };
+  for (int base = 0; base < p.B; base += 32) {
+    const int mine = base + lane, len_l = mine < p.B ? keys_of(p, mine) : p.Nq;
+    const bool few = len_l < p.Nq;
+    if (few && p.seqlens && blockIdx.x == 0 && threadIdx.x < 32) {
+      const int given = __ldg(p.seqlens + mine);
       if (given < 0 || given > (p.pps << p.page_shift)) record_status(p.status, kStatusCuSeqlens);
     }
-    // rows of the first Nq - len tokens see no key; the tiles that hold nothing else
-    const long long none = static_cast<long long>(p.Nq - len) * p.group;
-    const int dead = none >= rows ? rows : static_cast<int>(none / kRows * kRows);
-    const long long n = static_cast<long long>(dead) * p.Hkv * (D / 8);
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * blockDim.x) {
-      const unsigned r = static_cast<unsigned>(i / (D / 8));
-      const int row = static_cast<int>(r / static_cast<unsigned>(p.Hkv)), hk = static_cast<int>(r % static_cast<unsigned>(p.Hkv)), d = static_cast<int>(i % (D / 8)) * 8;
-      const size_t at = o_row(p, b, hk, row);
-      if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
+    const bool spread = few && static_cast<long long>(dead_rows(len_l)) * p.Hkv > 256;
+    unsigned todo = __ballot_sync(0xffffffffu, few && (spread || mine % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)));
+    const unsigned wide = __ballot_sync(0xffffffffu, spread);
+    while (todo) {
+      const int at_lane = __ffs(todo) - 1, b = base + at_lane;
+      todo &= todo - 1;
+      const bool all = (wide >> at_lane) & 1;
+      const long long n = static_cast<long long>(dead_rows(__shfl_sync(0xffffffffu, len_l, at_lane))) * p.Hkv * (D / 8);
+      const long long first = all ? static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x : threadIdx.x;
+      const long long step = all ? static_cast<long long>(gridDim.x) * blockDim.x : blockDim.x;
+      for (long long i = first; i < n; i += step) {
+        const unsigned r = static_cast<unsigned>(i / (D / 8));
+        const int row = static_cast<int>(r / static_cast<unsigned>(p.Hkv)), hk = static_cast<int>(r % static_cast<unsigned>(p.Hkv)), d = static_cast<int>(i % (D / 8)) * 8;
+        const size_t at = o_row(p, b, hk, row);
+        if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) store2<kFp16>(p.o, at * D + d + e, 0.f, 0.f, o_fp32 != 0);
-      if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
+        for (int e = 0; e < 8; e += 2) store2<kFp16>(p.o, at * D + d + e, 0.f, 0.f, o_fp32 != 0);
+        if (d == 0) p.lse[lse_row(p, b, hk, row)] = -INFINITY;
+      }
     }
   }
 }
@@ -318,6 +331,8 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x + 1;
   const Place place = find_place<kRows, kCombineThreads>(p, grid, c, scan);
+  // what follows this kernel must find the first one done, also where no border cuts a unit
+  if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (place.b < 0) return;
   const int shares = shares_of(p, place.total, grid);
   const Unit u = unit_at<kRows>(p, keys_of(p, place.b), place.off);
