@@ -13,14 +13,14 @@
 // overflows.  At the end O * 2^(mo - m) / l.  Both maxima are raised lazily (by more than 2^8 only).
 //
 // Rows: the G = Hq / Hkv query heads of a KV head times the Nq tokens, token-major, in tiles of 8, 16, 24 or 32:
-// keys are the M of the warp MMAs and rows their N, so that few rows waste little of the tensor pipe (a
-// 16-row M took 275 of its cycles per block where 8 rows take 138):
+// keys are the M of the warp MMAs and rows their N, so that few rows waste little of the tensor pipe (16 keys
+// against 8 rows take 138 of its cycles, against an M of 16 rows 275):
 //   S^T [16 keys x 8 rows]   = K [16 keys x D] Q^T,   O^T [D x 8 rows] += V^T [D x 16 keys] W^T [16 keys x 8 rows];
 // the weights go from the accumulator's layout to the operand's with a movmatrix.
-// Work is cut evenly over the CTAs (two to four per SM), whatever the lengths are: the
-// granules (64 keys) of all units (sequence, row tile, KV head) are numbered through, with a few more for
-// each unit's fixed cost, and CTA c takes the c-th equal share, which may begin and end inside a unit, and finds its place with a scan over the
-// lengths.  A unit that lies in one share is written at once; the pieces of the others go to the
+// Work is cut evenly over the CTAs (three per SM for up to 16 rows, else two), whatever the lengths are:
+// the granules (64 keys) of all units (sequence, row tile, KV head) are numbered through, with a few more
+// for each unit's fixed cost, and CTA c takes the c-th equal share, which may begin and end inside a unit,
+// and finds its place with a scan over the lengths.  A unit that lies in one share is written at once; the pieces of the others go to the
 // workspace (at most two per CTA) and are merged in order by a second kernel.  Warp w of the four takes every
 // fourth block of 16 keys: a block has one scale per pool and lies in one page, so a warp needs nothing
 // from the others until the end of a unit.  It streams its blocks (16 x D bytes of K and of V, contiguous in a
@@ -29,6 +29,10 @@
 // MMA a value takes is free as long as both operands agree, so no transposition is needed but of the
 // byte pairs of V (two PRMT per eight codes).  The ring's 16-byte chunks are swizzled so that both reads
 // are free of bank conflicts.  Warps and pieces are merged by their (m, l, mo, O).
+// What bounds it: up to 16 rows the reads (4 x 131072 keys, 32 heads: 191 us, 5.6 TB/s; without any arithmetic
+// 164 us), above that the instructions of two warps per scheduler, which depend on one another from the first
+// product over the softmax to the second (24 rows: 430 instructions a block of 16 keys in 1170 cycles; neither
+// fewer matrix products nor fewer conversions or exponentials make it shorter).
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -41,29 +45,31 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGranule = 64;  // keys: one block of 16 for each warp
+constexpr int kGranule = 64;  // keys
 constexpr int kUnitCost = 4;  // granules that a unit's fixed cost stands for (2 and 8: 102 and 96 us where 4 takes 94, B64 ragged 8192)
 constexpr int kMinShare = 8;
 constexpr int kWholeKeys = 1024;  // tables up to this many keys: a granule is a whole unit, nothing is merged
-constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (64 rows: 76 us here and 95 there,
-                               // 128 rows: 75 and 65; B8, 8 KV heads, D 128, 4096 and 2048 keys)
+constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (B8, 8 KV heads, D 128; 40 rows,
+                               // 8192 keys: 83 us here, 106 there; 64, 4096: 64 and 67; 96, 2048: 58 and 51)
 
 // CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.  Four of
 // one group leave 128 registers and less overlap inside a warp: 200 us where three take 193 (4 x 131072).
-template <int NG>
-constexpr int kPerSm = NG <= 2 ? 3 : 2;
-
 template <int D, int NG>
 struct Ring {
+  static constexpr int kPerSm = NG <= 2 ? 3 : 2;
   static constexpr int kRows = 8 * NG;
+  static constexpr bool kQSmem = NG >= 2;       // their registers are needed for O (with registers 71 us where this takes 64: 64 rows, 4096 keys, B8)
   static constexpr int kBlock = kKv8Block * D;  // bytes of 16 keys of K or V
   static constexpr int kStage = 2 * kBlock;
-  static constexpr int kRoom = (227 * 1024 / kPerSm<NG> - 2048) / kWarps - 128;
+  static constexpr int kQ = kQSmem ? kRows * (D * 2 + 4) : 0;
+  static constexpr int kRoom = (227 * 1024 / kPerSm - 2048 - kQ) / kWarps - 128;
   static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
   static constexpr int kWarp = kStages * kStage + 128;  // the stages, then (ks, vs) of each, 16 bytes apart
   static constexpr int kMerge = kWarps * kRows * (D + 3) * 4;
-  static constexpr int kSmem = kWarps * kWarp > kMerge ? kWarps * kWarp : kMerge;
+  static constexpr int kRings = kWarps * kWarp > kMerge ? kWarps * kWarp : kMerge;
+  static constexpr int kSmem = kRings + kQ;
   static_assert(kStages >= 3 && kStages * 16 <= 128, "stages, and their scales");
+  static_assert(kPerSm * (kSmem + 2048) <= 227 * 1024 + 1024, "room");
 };
 
 // Byte offset of 16-byte chunk ch of row r of a 16 x D block.  D = 128: a row is one 128-byte line; rows
@@ -131,7 +137,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 
 template <bool kFp16, bool kInt8, int D, int NG>
-__global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const __grid_constant__ AttParams p, const int o_fp32) {
+__global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kernel(const __grid_constant__ AttParams p, const int o_fp32) {
   using R = Ring<D, NG>;
   constexpr int kRows = R::kRows, kStages = R::kStages;
   constexpr int LD = D / 64;  // 16-byte pieces of a K row per lane
@@ -208,13 +214,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
       fetch(i, i, page);
     }
 
-    // queries: B operand, row 8 n + g, 16 values from d = 16 (t + 4 c); the scales of the rows 8 n + 2 t + e that
-    // this lane holds in the accumulators come from the lanes that read them
-    uint32_t qb[NG][LD][4][2];
+    // queries: B operand, row 8 n + g, 16 values from d = 16 (t + 4 c); in the order of halves_of, a word of K meets
+    // four values.  In registers, or (large tiles) in shared memory, as 16 bytes for each lane.
+    uint4* qsm = reinterpret_cast<uint4*>(smem + R::kRings);
+    float* qscale = reinterpret_cast<float*>(smem + R::kRings + kRows * D * 2);
+    uint4 qb[R::kQSmem ? 1 : NG][LD][2];
     float qs[NG][2];
     int lim[NG][2];
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
+    auto load_q = [&](int n, uint4 (&out)[LD][2]) {  // returns the factor that a score of row 8 n + g takes
       const int row = row0 + 8 * n + g;
       const bool in = row < rows;
       const size_t at = o_row(p, b, hk, in ? row : row0) * D;
@@ -253,15 +260,35 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
 #pragma unroll
       for (int c = 0; c < LD; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // the four values that a word of K meets, in the order of halves_of
-          qb[n][c][j][0] = kInt8 ? __byte_perm(w[c][2 * j], w[c][2 * j + 1], 0x5410) : w[c][2 * j];
-          qb[n][c][j][1] = kInt8 ? __byte_perm(w[c][2 * j], w[c][2 * j + 1], 0x7632) : w[c][2 * j + 1];
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t *x = w[c] + 4 * j;
+          out[c][j] = kInt8 ? make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                                         __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632))
+                            : make_uint4(x[0], x[1], x[2], x[3]);
         }
+      return down;
+    };
+    if constexpr (R::kQSmem) {
+      if (warp < NG) {
+        const float down = load_q(warp, qb[0]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = row0 + 8 * n + 2 * t + e;
-        qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
-        lim[n][e] = r < rows ? min(row_limit(p, len, r), hi) : 0;
+        for (int c = 0; c < LD; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) qsm[((warp * LD + c) * 2 + j) * 32 + lane] = qb[0][c][j];
+        if (t == 0) qscale[8 * warp + g] = down;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      float down = 0.f;
+      if constexpr (!R::kQSmem) down = load_q(n, qb[n]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // the rows that this lane holds in the accumulators
+        const int r = 8 * n + 2 * t + e;
+        if constexpr (R::kQSmem) qs[n][e] = qscale[r];
+        else qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
+        lim[n][e] = row0 + r < rows ? min(row_limit(p, len, row0 + r), hi) : 0;
       }
     }
 
@@ -296,12 +323,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NG>) kv8_attend_kernel(const 
         const uint4 x = *reinterpret_cast<const uint4*>(kb + ring_off<D>(g, t + 4 * c)), y = *reinterpret_cast<const uint4*>(kb + ring_off<D>(g + 8, t + 4 * c));
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3;
-          halves_of<kInt8>(xw[j], a0, a2);
-          halves_of<kInt8>(yw[j], a1, a3);
+        for (int j = 0; j < 2; ++j) {
+          uint32_t a[2][4];
 #pragma unroll
-          for (int n = 0; n < NG; ++n) mma_f16(sc[n], a0, a1, a2, a3, qb[n][c][j][0], qb[n][c][j][1]);
+          for (int i2 = 0; i2 < 2; ++i2) {
+            halves_of<kInt8>(xw[2 * j + i2], a[i2][0], a[i2][2]);
+            halves_of<kInt8>(yw[2 * j + i2], a[i2][1], a[i2][3]);
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const uint4 q = R::kQSmem ? qsm[((n * LD + c) * 2 + j) * 32 + lane] : qb[R::kQSmem ? 0 : n][c][j];
+            mma_f16(sc[n], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+            mma_f16(sc[n], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+          }
         }
       }
 
@@ -491,7 +525,7 @@ int groups_for(int Nq, int group) {
 template <bool kFp16, bool kInt8, int D, int NG>
 int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   using R = Ring<D, NG>;
-  constexpr int kCtas = kPerSm<NG> * kSms;
+  constexpr int kCtas = R::kPerSm * kSms;
   auto kern = kv8_attend_kernel<kFp16, kInt8, D, NG>;
   static PerContext<int> configured;
   int unused = 0;
@@ -528,7 +562,7 @@ int launch_rows(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
 
 size_t kv8_attend_ws_bytes(int B, int Nq, int Hq, int Hkv, int D) {
   if (on_chunk_kernel(Nq, Hq / Hkv)) return kv8_chunk_ws_bytes(D);
-  const int n = groups_for(Nq, Hq / Hkv), per_sm = n == 1 ? kPerSm<1> : n == 2 ? kPerSm<2> : n == 3 ? kPerSm<3> : kPerSm<4>;
+  const int n = groups_for(Nq, Hq / Hkv), per_sm = n <= 2 ? Ring<128, 1>::kPerSm : Ring<128, 3>::kPerSm;
   return static_cast<size_t>(2) * per_sm * kSms * 8 * n * (D + 1) * sizeof(float);
 }
 

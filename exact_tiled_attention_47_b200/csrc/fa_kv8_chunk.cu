@@ -79,7 +79,7 @@ struct ChunkBars {
   int abort_flag;
   // The pieces, walked by the conversion warps and handed on to the others (no keys left: the end).  With the walk in
   // every warp's registers it was spilled into the inner loops, whose local memory misses the small L1 that the
-  // tiles leave: 938 us where this takes 710 (chunk of 1024 behind 16384 keys, B2).
+  // tiles leave: 938 us where this took 710 (chunk of 1024 behind 16384 keys, B2).
   Piece piece[2];
   Walk walk[4];
   union {
