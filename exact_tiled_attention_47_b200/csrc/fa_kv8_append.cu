@@ -79,7 +79,7 @@ __device__ __forceinline__ float2 value2(uint32_t two) {  // two codes in the lo
 }
 
 template <bool kFp16, bool kInt8, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32, 3) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) kv8_append_kernel(const AppendParams p) {
   constexpr int LPR = D / 16;        // lanes per row
   constexpr int RPI = 32 / LPR;      // rows per step
   constexpr int IT = kKv8Block / RPI;
@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) kv8_append_kernel(const 
   // the block's new rows, 16 values of a row per lane and step (row r of the block: step r / RPI)
   const int c = lane % LPR;
   uint32_t raw[IT][8];
-  float top = 0.f;
-  bool odd = false;
+  uint32_t most = 0;  // the largest magnitudes: 16-bit values without their sign compare as integers, two at once
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int row = row0 + i * RPI + lane / LPR;
@@ -141,17 +140,25 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) kv8_append_kernel(const 
     raw[i][0] = u0.x; raw[i][1] = u0.y; raw[i][2] = u0.z; raw[i][3] = u0.w;
     raw[i][4] = u1.x; raw[i][5] = u1.y; raw[i][6] = u1.z; raw[i][7] = u1.w;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float2 f = unpack2<kFp16>(raw[i][w]);
-      const float ax = fabsf(f.x), ay = fabsf(f.y);
-      const bool bx = !(ax < INFINITY), by = !(ay < INFINITY);  // infinity or NaN
-      odd |= bx || by;
-      top = fmaxf(top, fmaxf(bx ? 0.f : ax, by ? 0.f : ay));
-    }
+    for (int w = 0; w < 8; ++w) most = __vmaxu2(most, raw[i][w] & 0x7FFF7FFFu);
   }
+  most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
+  float top = unpack2<kFp16>(most).x;
+  const bool finite = most < (kFp16 ? 0x7C00u : 0x7F80u);
+  if (!finite) {  // the block holds an infinity or a NaN, which the maximum passes over
+    top = 0.f;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (__any_sync(0xffffffffu, odd) && lane == 0) record_status(p.status, kStatusNonFinite);
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 f = unpack2<kFp16>(raw[i][w]);
+        const float ax = fabsf(f.x), ay = fabsf(f.y);
+        top = fmaxf(top, fmaxf(ax < INFINITY ? ax : 0.f, ay < INFINITY ? ay : 0.f));
+      }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) record_status(p.status, kStatusNonFinite);
+  }
 
   float scale = block_scale<kInt8>(top);
   const bool older = first > row0;  // rows of an earlier append share the block
@@ -181,6 +188,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) kv8_append_kernel(const 
   __syncwarp();
   if (lane == 0) *scale_at = scale;
   const float inv = exact_reciprocal(scale);
+  if (finite && inv != 0.f) {  // every value is at most qmax * scale
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int row = row0 + i * RPI + lane / LPR;
+      if (row < lo || row >= hi) continue;
+      uint32_t out[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 e = unpack2<kFp16>(raw[i][2 * w]), f = unpack2<kFp16>(raw[i][2 * w + 1]);
+        if constexpr (kInt8) {  // x / scale + 1.5 * 2^23 is rounded to an integer, whose low byte is the code
+          constexpr float kRound = 12582912.f;
+          const uint32_t lo2 = __byte_perm(__float_as_uint(fmaf(e.x, inv, kRound)), __float_as_uint(fmaf(e.y, inv, kRound)), 0x0040);
+          const uint32_t hi2 = __byte_perm(__float_as_uint(fmaf(f.x, inv, kRound)), __float_as_uint(fmaf(f.y, inv, kRound)), 0x0040);
+          out[w] = __byte_perm(lo2, hi2, 0x5410);
+        } else {
+          out[w] = __byte_perm(code2<false>(e.x * inv, e.y * inv), code2<false>(f.x * inv, f.y * inv), 0x5410);
+        }
+      }
+      *reinterpret_cast<uint4*>(codes + (row - row0) * D + c * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int row = row0 + i * RPI + lane / LPR;
