@@ -152,6 +152,8 @@ def append_kv8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_
     B, Nt, Hkv, D = shape = k.shape
     dev, dtype = k.device, k.dtype
     num_pages, _, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, Hkv, D, dev)
+    if seqlens_k is None:
+        raise ValueError("seqlens_k: an int32 tensor [B], the lengths with the new rows included")
     if new_lens is not None:
         check_tensor("new_lens", new_lens, _INT32, (B,), dev)
     if v.dtype is not dtype or v.shape != shape or v.device != dev:

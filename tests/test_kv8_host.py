@@ -144,6 +144,8 @@ def test_helpers_refuse_what_is_not_on_a_gpu_or_not_alike():
         fa.append_kv8(k, k.bfloat16(), kp, kp, ks, ks, table, lens)
     with pytest.raises(ValueError, match="heads"):
         fa.append_kv8(k[:, :, :1], k[:, :, :1], kp, kp, ks, ks, table, lens)
+    with pytest.raises(ValueError, match="seqlens_k"):
+        fa.append_kv8(k, k, kp, kp, ks, ks, table, None)
     with pytest.raises(ValueError, match="new_lens"):
         fa.append_kv8(k, k, kp, kp, ks, ks, table, lens, new_lens=lens.long())
     refs = torch.zeros(4, dtype=torch.int32)
