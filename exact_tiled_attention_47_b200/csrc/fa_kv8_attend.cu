@@ -107,8 +107,9 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 template <bool kInt8>
 __device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (kInt8) {
-    lo = (w & 0x00FF00FFu) ^ 0x64806480u;
-    hi = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    w ^= 0x80808080u;
+    lo = __byte_perm(w, 0x64646464u, 0x4240);
+    hi = __byte_perm(w, 0x64646464u, 0x4341);
     const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
     const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&lo), off), y = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
     lo = *reinterpret_cast<const uint32_t*>(&x);
