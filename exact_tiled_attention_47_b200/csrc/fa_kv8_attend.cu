@@ -29,8 +29,8 @@
 // MMA a value takes is free as long as both operands agree, so no transposition is needed but of the
 // byte pairs of V (two PRMT per eight codes).  The ring's 16-byte chunks are swizzled so that both reads
 // are free of bank conflicts.  Warps and pieces are merged by their (m, l, mo, O).
-// What bounds it: up to 16 rows the reads (4 x 131072 keys, 32 heads: 191 us, 5.6 TB/s; without any arithmetic
-// 164 us), above that the instructions of two warps per scheduler, which depend on one another from the first
+// What bounds it: up to 16 rows the reads (4 x 131072 keys, 32 heads, int8: 176 us, 6.1 TB/s, e4m3 185; without
+// any arithmetic 164 us), above that the instructions of two warps per scheduler, which depend on one another from the first
 // product over the softmax to the second (24 rows: 430 instructions a block of 16 keys in 1170 cycles; neither
 // fewer matrix products nor fewer conversions or exponentials make it shorter).
 #include <algorithm>
@@ -53,7 +53,7 @@ constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen
                                // 8192 keys: 83 us here, 106 there; 64, 4096: 64 and 67; 96, 2048: 58 and 51)
 
 // CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.  Four of
-// one group leave 128 registers and less overlap inside a warp: 200 us where three take 193 (4 x 131072).
+// one group left 128 registers and less overlap inside a warp: 200 us where three took 193 (4 x 131072, int8).
 template <int D, int NG>
 struct Ring {
   static constexpr int kPerSm = NG <= 2 ? 3 : 2;
@@ -103,7 +103,8 @@ template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Four codes as fp16 pairs: e4m3 codes (0, 1) and (2, 3) of the word by the hardware's conversion (2.9 clocks
-// per warp and pair), int8 codes (0, 2) and (1, 3): code + 128 in the mantissa of 1024, less 1152, all exact.
+// per warp and pair), int8 codes (0, 2) and (1, 3): code + 128 in the mantissa of 1024, less 1152, all exact
+// (three byte permutes and logic operations per word; with masks and shifts five, and 194 us where 4 x 131072 take 176).
 template <bool kInt8>
 __device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (kInt8) {
