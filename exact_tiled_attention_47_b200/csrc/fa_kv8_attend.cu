@@ -49,6 +49,8 @@ constexpr int kGranule = 64;  // keys
 constexpr int kUnitCost = 4;  // granules that a unit's fixed cost stands for (2 and 8: 102 and 96 us where 4 takes 94, B64 ragged 8192)
 constexpr int kMinShare = 8;
 constexpr int kWholeKeys = 1024;  // tables up to this many keys: a granule is a whole unit, nothing is merged
+constexpr int kManyPieces = 16;  // CTAs per unit from which on tiles of up to 16 rows are merged by many CTAs (32: 4 x 32768 keys,
+                                 // 4 heads 37 us where 16 takes 34; 24 rows, 8 x 20221: 39 us with them, 33 without)
 constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (B8, 8 KV heads, D 128; 40 rows,
                                // 8192 keys: 83 us here, 106 there; 64, 4096: 64 and 67; 96, 2048: 58 and 51)
 
@@ -545,8 +547,12 @@ int launch_t(const Attend8Args& a, AttParams& p, cudaStream_t stream) {
   const long long most = ((cap + p.granule - 1) / p.granule + p.over) * p.B * p.Hkv * p.tiles;
   const int grid = static_cast<int>(std::min<long long>(kCtas, (most + p.least - 1) / p.least));
   kern<<<grid, kThreads, R::kSmem, stream>>>(p, a.o_fp32);
-  if (p.over && grid > 1)
-    if (const int e = launch_combine8<kFp16, D, R::kRows>(p, a.o_fp32, grid, stream)) return e;
+  if (p.over && grid > 1) {
+    const bool many = NG <= 2 && static_cast<long long>(p.B) * p.Hkv * p.tiles * kManyPieces <= grid;
+    const int e = many ? launch_combine8<kFp16, D, R::kRows, NG <= 2>(p, a.o_fp32, grid, stream)
+                       : launch_combine8<kFp16, D, R::kRows>(p, a.o_fp32, grid, stream);
+    if (e != 0) return e;
+  }
   return static_cast<int>(cudaGetLastError());
 }
 

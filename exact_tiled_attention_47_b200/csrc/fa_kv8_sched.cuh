@@ -317,16 +317,18 @@ __device__ __forceinline__ void write_tiles_without_keys(const AttParams& p, int
 // Merges the pieces of the units that lie in more than one share.  CTA i looks at the border between
 // shares i and i + 1 and takes the unit it cuts, if no earlier border cuts the same one: piece 0 is the
 // end of share i, the others are the beginnings of shares i + 1, i + 2, ...  O = sum_s exp(lse_s - M) o_s /
-// sum_s exp(lse_s - M), LSE = M + ln of that sum; two rows to a warp, eight of a tile to a CTA (long
-// contexts of few heads come in a hundred pieces: one after another they took 100 us).
+// sum_s exp(lse_s - M), LSE = M + ln of that sum; two rows to a warp, eight of a tile to a CTA.  kMany, for long
+// contexts of few heads, which come in a hundred pieces and more: two rows to a CTA, whose warps take a
+// quarter of the pieces each (2 x 95246 keys, 10 rows: 58 us without it, 36 with it).
 constexpr int kCombineThreads = 128;
-template <int kRows>
-constexpr int kCombineRows = 8;
+template <bool kMany>
+constexpr int kCombineRows = kMany ? 2 : 8;
 
-template <bool kFp16, int D, int kRows>
+template <bool kFp16, int D, int kRows, bool kMany>
 __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttParams p, const int o_fp32, const int grid) {
-  constexpr int kPart = kCombineRows<kRows>, kWarps = kCombineThreads / 32;
-  constexpr int PER = D / 32, RPW = kPart / kWarps;  // rows of a warp, all under way at once
+  constexpr int kPart = kCombineRows<kMany>, kWarps = kCombineThreads / 32;
+  constexpr int PER = D / 32, RPW = 2;        // rows of a warp, both under way at once
+  constexpr int kStride = kMany ? 1 : kWarps;  // between them
   __shared__ ScanMem<kCombineThreads> scan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x + 1;
@@ -345,12 +347,14 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
   if (part >= rows) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
 
+  const int each = kMany ? (pieces + kWarps) / kWarps : pieces + 1;  // pieces of this warp
+  const int from = kMany ? warp * each : 0, to = min(from + each, pieces + 1);
   float M[RPW], sum[RPW], acc[RPW][PER];
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
-    const int row = part + warp + i * kWarps;
+    const int row = part + (kMany ? 0 : warp) + i * kStride;
     M[i] = kNone;
-    for (int s = lane; s <= pieces && row < rows; s += 32) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
+    for (int s = from + lane; s < to && row < rows; s += 32) M[i] = fmaxf(M[i], p.ws_l[slot(s) + row] * kLog2e);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], o));
     sum[i] = 0.f;
@@ -358,15 +362,15 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
     for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
   }
   // eight pieces' loads are under way at once
-  for (int s0 = 0; s0 <= pieces; s0 += 8) {
+  for (int s0 = from; s0 < to; s0 += 8) {
     float w[RPW][8];
     float2 x[RPW][8][PER / 2];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
 #pragma unroll
       for (int i = 0; i < RPW; ++i) {
-        const int row = part + warp + i * kWarps;
-        const bool in = s0 + k <= pieces && row < rows;
+        const int row = part + (kMany ? 0 : warp) + i * kStride;
+        const bool in = s0 + k < to && row < rows;
         const size_t at = slot(in ? s0 + k : 0) + (in ? row : 0);
         w[i][k] = in ? p.ws_l[at] : -INFINITY;
         const float2* src = reinterpret_cast<const float2*>(p.ws_o + at * D) + lane * (PER / 2);
@@ -386,9 +390,36 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
         }
       }
   }
+  if constexpr (kMany) {  // the warps' sums, in order
+    __shared__ float part_m[kWarps][RPW], part_sum[kWarps][RPW], part_acc[kWarps][RPW][D];
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      part_m[warp][i] = M[i];
+      part_sum[warp][i] = sum[i];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) part_acc[warp][i][lane * PER + e] = acc[i][e];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M[i] = fmaxf(M[i], part_m[w][i]);
+      sum[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(part_m[w][i] - M[i]);
+        sum[i] = fmaf(f, part_sum[w][i], sum[i]);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[i][e] = fmaf(f, part_acc[w][i][lane * PER + e], acc[i][e]);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
-    const int row = part + warp + i * kWarps, rr = u.tile * kRows + row;
+    const int row = part + (kMany ? 0 : warp) + i * kStride, rr = u.tile * kRows + row;
     if (row >= rows) continue;
     const bool none = M[i] == kNone;
     const float inv = none ? 0.f : 1.f / sum[i];
@@ -402,19 +433,19 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
 }
 
 // Launched while the first kernel still runs: it finds its place meanwhile and waits for the pieces.
-template <bool kFp16, int D, int kRows>
+template <bool kFp16, int D, int kRows, bool kMany = false>
 int launch_combine8(const AttParams& p, int o_fp32, int grid, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const long long rows = std::min<long long>(kRows, static_cast<long long>(p.Nq) * p.group);  // of the largest tile
-  cfg.gridDim = dim3(grid - 1, static_cast<unsigned>((rows + kCombineRows<kRows> - 1) / kCombineRows<kRows>));
+  cfg.gridDim = dim3(grid - 1, static_cast<unsigned>((rows + kCombineRows<kMany> - 1) / kCombineRows<kMany>));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kFp16, D, kRows>, p, o_fp32, grid));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kFp16, D, kRows, kMany>, p, o_fp32, grid));
 }
 
 }  // namespace

@@ -86,6 +86,23 @@ def test_shares_of_ragged_batches(seed, Nq, G):
     close(o, lse, plain(q, g, lens, kind), (B, top))
 
 
+@pytest.mark.parametrize("Nq,G,D,kind", [(1, 1, 128, "e4m3"), (3, 5, 128, "int8"), (1, 16, 64, "e4m3"), (4, 9, 128, "e4m3")])
+def test_units_of_many_pieces(Nq, G, D, kind):
+    # few heads and long contexts: a unit is cut into a hundred pieces, beside one of a single key and an empty one
+    import exact_tiled_attention_47_b200 as fa
+    rng = np.random.default_rng(900 + G)
+    lens = [60000, 1, 20011, 0]
+    cache = make_cache(rng, lens, 1, D, 64, kind)
+    q, _ = rounded(rng, (4, Nq, G, D), "bf16", 0.3)
+    g = to_gpu(cache, kind)
+    o, lse = fa.attend_kv8(q, *g, torch.tensor(lens, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == 0
+    close(o, lse, plain(q, g, lens, kind), lens)
+    again, _ = fa.attend_kv8(q, *g, torch.tensor(lens, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    assert torch.equal(o, again)
+
+
 @pytest.mark.parametrize("Nq,G", [(1, 2), (40, 3)])
 def test_more_items_than_threads(Nq, G):
     # the scan over the lengths takes several steps
