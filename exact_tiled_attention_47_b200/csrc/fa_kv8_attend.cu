@@ -10,7 +10,9 @@
 //   mo   = running max of s_j + log2 vs(j), O = sum 2^(s_j + log2 vs(j) - mo) cv_j
 // O has a maximum of its own: its weights carry the value scales, so they are rounded to fp16 (11
 // significant bits) relative to the largest contribution whatever the scales are, and nothing
-// overflows.  At the end O * 2^(mo - m) / l.  Both maxima are raised lazily (by more than 2^8 only).
+// overflows.  mo is kept as dm = mo - m and a weight taken as 2^((s_j - m) + (log2 vs(j) - dm)), from the very s_j - m
+// that the row sum takes: with an mo of its own, rounded at the size of the scores, the two drift apart by half a step of
+// the score (O 4 % off at scores of 10^6).  At the end O * 2^dm / l.  Both maxima are raised lazily (by more than 2^8 only).
 //
 // Rows: the G = Hq / Hkv query heads of a KV head times the Nq tokens, token-major, in tiles of 8, 16, 24 or 32:
 // keys are the M of the warp MMAs and rows their N, so that few rows waste little of the tensor pipe (16 keys
@@ -297,12 +299,13 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
     }
 
     float o[NG][MT][4];
-    float m[NG][2], mo[NG][2], l[NG][2];
+    float m[NG][2], dm[NG][2], l[NG][2];  // (before the first key dm is any finite number)
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = kNone;
+      m[n][0] = m[n][1] = kNone;
+      dm[n][0] = dm[n][1] = 0.f;
       l[n][0] = l[n][1] = 0.f;
     }
 
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
           f[n][e] = qs[n][e] * ks;
           const float top = fmaxf(sc[n][e], sc[n][2 + e]);
           mx[n][e] = top == -INFINITY ? -INFINITY : top * f[n][e];  // (-inf stays what it is where the scale is zero)
-          past |= mx[n][e] > fminf(m[n][e], mo[n][e] - lv) + kLazy;
+          past |= mx[n][e] > m[n][e] + fminf(kLazy, dm[n][e] - (lv - kLazy));
         }
       }
       // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks; one vote for
@@ -373,19 +376,21 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
             float top = mx[n][e];
 #pragma unroll
             for (int s2 = 4; s2 <= 16; s2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s2));
-            if (top > m[n][e]) {
-              l[n][e] *= ex2(m[n][e] - top);
+            if (top > m[n][e]) {  // (mo stays what it is)
+              const float by = m[n][e] - top;
+              l[n][e] *= ex2(by);
+              dm[n][e] += by;
               m[n][e] = top;
             }
-            const float mv = top + lv;
-            if (mv > mo[n][e]) {
-              const float a = ex2(mo[n][e] - mv);
+            const float mv = (top - m[n][e]) + lv;
+            if (mv > dm[n][e]) {
+              const float a = ex2(dm[n][e] - mv);
 #pragma unroll
               for (int i2 = 0; i2 < MT; ++i2) {
                 o[n][i2][e] *= a;
                 o[n][i2][2 + e] *= a;
               }
-              mo[n][e] = mv;
+              dm[n][e] = mv;
             }
           }
       }
@@ -393,15 +398,14 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
       for (int n = 0; n < NG; ++n) {
         float p2[4], w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p2[e] = fmaf(sc[n][e], f[n][e & 1], -m[n][e & 1]);
-          w[e] = fmaf(sc[n][e], f[n][e & 1], lv - mo[n][e & 1]);
-        }
+        for (int e = 0; e < 4; ++e) p2[e] = fmaf(sc[n][e], f[n][e & 1], -m[n][e & 1]);
         if (edge) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (sc[n][e] == -INFINITY) p2[e] = w[e] = -INFINITY;
+            if (sc[n][e] == -INFINITY) p2[e] = -INFINITY;
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = p2[e] + (lv - dm[n][e & 1]);
         l[n][0] += ex2(p2[0]) + ex2(p2[2]);
         l[n][1] += ex2(p2[1]) + ex2(p2[3]);
         wb[n][0] = transpose8x8(pack2<true>(ex2(w[0]), ex2(w[1])));  // keys 0..7 of the block
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
     cp_wait<0>();
     __syncthreads();
 
-    // merge of the four warps through shared memory: O [warp][row][d], then m, l, mo [warp][row]; a row's
+    // merge of the four warps through shared memory: O [warp][row][d], then m, l, dm [warp][row]; a row's
     // factors (one per warp) and its place take the room of the latter
     float* ro = reinterpret_cast<float*>(smem);
     float* rm = ro + kWarps * kRows * D;
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
         if (g == 0) {
           rm[row] = m[n][e];
           rl[row] = sum;
-          rw[row] = mo[n][e];
+          rw[row] = dm[n][e];
         }
 #pragma unroll
         for (int i = 0; i < MT; i += 2)
@@ -471,14 +475,16 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
       const int rr = row0 + tid;
       float M = kNone, W = kNone, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, rm[w * kRows + tid]);
-        W = fmaxf(W, rw[w * kRows + tid]);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, rm[w * kRows + tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {  // mo - M of each warp, and the largest
+        const float d = rw[w * kRows + tid] += rm[w * kRows + tid] - M;
+        W = fmaxf(W, d);
       }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += ex2(rm[w * kRows + tid] - M) * rl[w * kRows + tid];
       const bool none = M == kNone;
-      const float f = none ? 0.f : ex2(W - M) / sum;
+      const float f = none ? 0.f : ex2(W) / sum;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) rw[w * kRows + tid] = ex2(rw[w * kRows + tid] - W) * f;
       const float ls = none ? -INFINITY : (M + lg2(sum)) * kLn2;

@@ -1,0 +1,77 @@
+"""Attention over the 8-bit cache where scores are large, far apart, or not numbers.
+
+All caches here are one sequence and one KV head on pages in order, so that the right answer can be written down: both
+kernels, with units that lie in one share (up to 1024 keys of table for the first, 512 for the second) and cut ones.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from test_gpu_kv8 import CODE, codes_to
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+D, PAGE = 64, 16
+# keys, tokens, heads of a group: first kernel whole, cut, cut into many pieces; tcgen05 kernel whole, cut
+CASES = [(600, 1, 4), (5000, 3, 12), (40000, 1, 3), (400, 100, 2), (3000, 150, 2)]
+IDS = [f"n{n}q{q}g{g}" for n, q, g in CASES]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_tiled_attention_47_b200 import build
+    build.build()
+    import exact_tiled_attention_47_b200 as fa
+    fa.fa_device_status(clear=True)
+    yield
+    assert fa.fa_device_status(clear=True) == 0
+
+
+def attend(q, k, v, ks, vs, kind, scale=None):
+    """O [Nq, G, D], LSE [G, Nq] in fp64 from values k, v [n, D] that codes hold exactly, one scale per 16 of them."""
+    import exact_tiled_attention_47_b200 as fa
+    n = len(k)
+    pages = -(-n // PAGE)
+
+    def pool(x):
+        full = np.zeros((pages * PAGE, D))
+        full[:n] = x
+        codes = oracle.kv8.encode(full, kind)
+        assert np.array_equal(oracle.kv8.decode(codes, kind)[:n], x)
+        return codes_to(codes.reshape(pages, 1, PAGE, D), kind)
+
+    def scales(x):
+        return torch.from_numpy(np.broadcast_to(x, pages).astype(np.float32).reshape(pages, 1, 1)).cuda()
+
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    o, lse = fa.attend_kv8(q.cuda()[None], pool(k), pool(v), scales(ks), scales(vs), table, lens, scale=scale, out_dtype=torch.float32)
+    return o[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+@pytest.mark.parametrize("kind", list(CODE))
+@pytest.mark.parametrize("score", [1e3, 1e5, 1e6])
+def test_one_key_far_ahead_at_large_scores(case, kind, score):
+    # Key 5 has the score given, every other one half of it: the softmax is 1 at key 5 and 0 elsewhere, so O is that key's
+    # value.  Its weight is off by 2^-11 (rounded to fp16) and by the exponentials and the merges (2^-22 each, a handful,
+    # below 2^-18 in all), O once more by its rounding to fp32; nothing of it grows with the score.  The LSE is the score:
+    # six roundings or constants of 2^-24 relative, 2^-21 with room.
+    n, Nq, G = case
+    rng = np.random.default_rng(n)
+    k = np.zeros((n, D))
+    k[:, 0], k[5, 0] = 60.0, 120.0
+    v = rng.integers(1, 8, (n, D)).astype(np.float64)
+    q = torch.zeros((Nq, G, D), dtype=torch.float16)
+    q[..., 0] = 1.0
+    scale = float(np.float32(score / 120.0 * 1.0314159))
+    o, lse = attend(q, k, v, 1.0, 0.37, kind, scale)
+    want = v[5] * float(np.float32(0.37))
+    assert np.all(np.abs(o - want) <= want * (2.0 ** -11 + 2.0 ** -18)), np.abs(o / want - 1).max()
+    assert np.all(np.abs(lse - 120.0 * scale) <= 2.0 ** -21 * 120.0 * scale)
