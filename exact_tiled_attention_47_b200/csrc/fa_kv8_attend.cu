@@ -8,9 +8,9 @@
 //                                                 8-bit significands are exact in fp16)
 //   m    = running max of s_j, l = sum 2^(s_j - m)
 //   mo   = running max of s_j + log2 vs(j), O = sum 2^(s_j + log2 vs(j) - mo) cv_j
-// O has a maximum of its own: its weights carry the value scales, so they are rounded to fp16 (11
-// significant bits) relative to the largest contribution whatever the scales are, and nothing
-// overflows.  mo is kept as dm = mo - m and a weight taken as 2^((s_j - m) + (log2 vs(j) - dm)), from the very s_j - m
+// O has a maximum of its own: its weights carry the value scales, so their rounding to fp16 is relative to the largest
+// contribution whatever the scales are, and nothing overflows: 11 significant bits down to 2^-21 of the largest one, fewer
+// down to 2^-32 (kHead).  mo is kept as dm = mo - m and a weight taken as 2^((s_j - m) + (log2 vs(j) - dm)), from the very s_j - m
 // that the row sum takes: with an mo of its own, rounded at the size of the scores, the two drift apart by half a step of
 // the score (O 4 % off at scores of 10^6).  At the end O * 2^dm / l.  Both maxima are raised lazily (by more than 2^8 only).
 //
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
     }
 
     float o[NG][MT][4];
-    float m[NG][2], dm[NG][2], l[NG][2];  // (before the first key dm is any finite number)
+    float m[NG][2], dm[NG][2], l[NG][2];  // dm: mo - m - kHead (before the first key any finite number)
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
           f[n][e] = qs[n][e] * ks;
           const float top = fmaxf(sc[n][e], sc[n][2 + e]);
           mx[n][e] = top == -INFINITY ? -INFINITY : top * f[n][e];  // (-inf stays what it is where the scale is zero)
-          past |= mx[n][e] > m[n][e] + fminf(kLazy, dm[n][e] - (lv - kLazy));
+          past |= mx[n][e] > m[n][e] + fminf(kLazy, dm[n][e] - (lv - (kHead + kLazy)));
         }
       }
       // the maxima are raised when a score of any lane passes them by more than 2^8 (rare after a few blocks; one vote for
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
               dm[n][e] += by;
               m[n][e] = top;
             }
-            const float mv = (top - m[n][e]) + lv;
+            const float mv = (top - m[n][e]) + (lv - kHead);
             if (mv > dm[n][e]) {
               const float a = ex2(dm[n][e] - mv);
 #pragma unroll
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
         for (int e = 0; e < 4; ++e) w[e] = p2[e] + (lv - dm[n][e & 1]);
         l[n][0] += ex2(p2[0]) + ex2(p2[2]);
         l[n][1] += ex2(p2[1]) + ex2(p2[3]);
-        wb[n][0] = transpose8x8(pack2<true>(ex2(w[0]), ex2(w[1])));  // keys 0..7 of the block
-        wb[n][1] = transpose8x8(pack2<true>(ex2(w[2]), ex2(w[3])));  // keys 8..15
+        wb[n][0] = transpose8x8(pack_weights(ex2(w[0]), ex2(w[1])));  // keys 0..7 of the block
+        wb[n][1] = transpose8x8(pack_weights(ex2(w[2]), ex2(w[3])));  // keys 8..15
       }
 
       // O^T += V^T W^T: this lane's keys 2t, 2t + 1 of both halves of the block, D / 8 columns from d = (D / 8) g;
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
 #pragma unroll
         for (int i = 0; i < MT; i += 2)
           *reinterpret_cast<float4*>(ro + merge_at<D>(row, (D / 8) * g + 2 * i)) =
-              make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+              make_float4(o[n][i][e] * kUnhead, o[n][i][2 + e] * kUnhead, o[n][i + 1][e] * kUnhead, o[n][i + 1][2 + e] * kUnhead);
       }
     __syncthreads();
     const int slot = 2 * blockIdx.x + pc.slot;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += ex2(rm[w * kRows + tid] - M) * rl[w * kRows + tid];
       const bool none = M == kNone;
-      const float f = none ? 0.f : ex2(W) / sum;
+      const float f = none ? 0.f : ex2(W + kHead) / sum;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) rw[w * kRows + tid] = ex2(rw[w * kRows + tid] - W) * f;
       const float ls = none ? -INFINITY : (M + lg2(sum)) * kLn2;

@@ -9,7 +9,7 @@
 //     them (128-byte rows, 16-byte chunks XOR-ed with the row).  It also brings the queries to fp16 (bf16
 //     rows times a power of two) and the scales to shared memory.
 //   - a tile has eight blocks of 16 keys with a scale each.  With f = q scale * ks and the maxima m (of the
-//     scores) and mo (of score + log2 vs), a weight is w = 2^(s f + log2 vs - mo): one fma and one ex2 as
+//     scores) and mo (of score + log2 vs, less kHead), a weight is w = 2^(s f + log2 vs - mo): one fma and one ex2 as
 //     before, with other constants for each block; the row sum takes it back to 2^(s f - m) with the factor
 //     2^(mo - m - log2 vs) in the same instruction that adds it.  Where a block's vs is 2^64 or more below
 //     the row's largest contribution, that factor could meet a weight that was flushed to zero: then the
@@ -176,7 +176,7 @@ __device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, uint
       } else {
         acc0 = f2_fma(pe, d2v, acc0);
       }
-      pk[h * 8 + i] = pack2<true>(p0, p1);
+      pk[h * 8 + i] = pack_weights(p0, p1);
     }
   }
 }
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       // keys visible to this row, and to every row of the tile (rows behind the last one are zeros and see all)
       const int lim = row < rows ? min(row_limit(p, pc.len, row), pc.hi) : pc.hi;
       const int all = min(row_limit(p, pc.len, tile0), pc.hi);
-      float m = kNone, mo = kNone, qs = 0.f;
+      float m = kNone, mo = kNone, qs = 0.f;  // (mo: less kHead)
       uint64_t lsum = f2(0.f, 0.f);
       for (int j = 0; j < blocks; ++j) {
         if (!(ok = warp_wait(&bars->s_full[t], (c0 + j) & 1, abort_flag, p.status))) break;
@@ -536,13 +536,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
         }
         // The maxima are raised when they are exceeded by more than 2^8 (warp-uniform); O waits below until
         // the product before has landed.
-        const bool past = mx > m + kLazy || mv > mo + kLazy;
+        const bool past = mx > m + kLazy || mv > mo + (kHead + kLazy);
         float alpha = 1.f;
         bool rescale = false;
         if (__any_sync(0xffffffffu, past)) {
           rescale = j > 0;
           if (past) {
-            const float m_new = fmaxf(m, mx), mo_new = fmaxf(mo, mv), a = ex2(m - m_new);
+            const float m_new = fmaxf(m, mx), mo_new = fmaxf(mo, mv - kHead), a = ex2(m - m_new);
             alpha = ex2(mo - mo_new);
             float l0, l1;
             f2_split(lsum, l0, l1);
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       float l0, l1;
       f2_split(lsum, l0, l1);
       const bool none = m == kNone;
-      const float f = none ? 0.f : ex2(mo - m) / (l0 + l1), ls = none ? -INFINITY : (m + lg2(l0 + l1)) * kLn2;
+      const float f = none ? 0.f : ex2(mo - m + kHead) / (l0 + l1), ls = none ? -INFINITY : (m + lg2(l0 + l1)) * kLn2;
       const int slot = 2 * blockIdx.x + pc.slot;
       const size_t at = pc.whole ? o_row(p, pc.b, pc.hk, min(row, rows - 1)) : static_cast<size_t>(slot) * kUnitRows + t * kBM + r;
       const bool st = row < rows && idx_ok(p.status, at, 1, pc.whole ? static_cast<long long>(p.B) * p.Nq * p.Hq : 2LL * gridDim.x * kUnitRows);
@@ -614,7 +614,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t orr[32];
         tmem_ld32_sync(lane_base + C::col_o(t) + ch * 32, orr);
-        const float* x = reinterpret_cast<const float*>(orr);
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(orr[i]) * kUnhead;
         if (!st) {
           // nothing of this row is stored (the loads of O are collective)
         } else if (!pc.whole || o_fp32) {

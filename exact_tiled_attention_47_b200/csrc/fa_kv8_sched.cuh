@@ -13,6 +13,11 @@ namespace {
 
 constexpr int kSms = 148;
 constexpr float kLazy = 8.f;     // log2 units by which a maximum may be exceeded before it is raised
+// Weights of O are 2^kHead times the contribution relative to the largest one, so they stay below 2^(kHead + kLazy) = 2^15, half
+// of what fp16 holds, and a contribution counts down to 2^-32 of the largest (with a unit of 1 it was lost below
+// 2^-25, while the row sum had it: many small keys beside a large one of no value were gone from O).
+constexpr float kHead = 7.f;
+constexpr float kUnhead = 0x1p-7f;
 constexpr float kNone = -1e30f;  // a maximum over nothing (finite, so that differences with -inf are defined)
 constexpr int kStatusPageTable = 12;  // FA_ERR_PAGE_TABLE
 
@@ -67,6 +72,14 @@ inline AttParams params_of(const Attend8Args& a) {
 
 // 2^e as fp32, e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Two weights as fp16.  Beyond scores of 10^7, where a step of the score is a factor of two and more, they could pass
+// its range: the largest finite value then.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 template <bool kFp16>
 __device__ __forceinline__ void store2(void* o, size_t at, float a, float b, bool f32) {

@@ -75,3 +75,34 @@ def test_one_key_far_ahead_at_large_scores(case, kind, score):
     want = v[5] * float(np.float32(0.37))
     assert np.all(np.abs(o - want) <= want * (2.0 ** -11 + 2.0 ** -18)), np.abs(o / want - 1).max()
     assert np.all(np.abs(lse - 120.0 * scale) <= 2.0 ** -21 * 120.0 * scale)
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+@pytest.mark.parametrize("kind", list(CODE))
+@pytest.mark.parametrize("gap", [18.0, 20.0])
+def test_small_keys_beside_large_ones_of_no_value(case, kind, gap):
+    # Keys 3, 19, 35 and 51 (one in each of the first four blocks, so every warp that starts there meets one) are `gap` ahead
+    # and have V = 0: all of O is what the others add, each with exp(-gap) of the weight (2^-26 and 2^-28.9).
+    # Off by: 2^-11 where a weight is a normal fp16 number; else at most 2^-32 of the largest contribution (in values: qmax
+    # times the scale times that key's share) for each key; 2^-20 + keys 2^-24 for exponentials and fp32 sums, 2 ds for
+    # scores off by ds = 2 (D + 8) 2^-24 gap; then the rounding to fp32.
+    n, Nq, G = case
+    rng = np.random.default_rng(n + 1)
+    qmax = oracle.kv8.QMAX[kind]
+    k = np.zeros((n, D))
+    v = rng.integers(14, 29, (n, D)) * 16.0 if kind == "e4m3" else rng.integers(64, 128, (n, D)) * 1.0
+    v = oracle.kv8.decode(oracle.kv8.encode(v, kind), kind)
+    big = [3, 19, 35, 51]
+    k[big, 0], v[big] = gap, 0.0
+    q = torch.zeros((Nq, G, D), dtype=torch.float16)
+    q[..., 0] = 8.0
+    o, lse = attend(q, k, v, 1.0, 1.0, kind, 0.125)
+    for i in range(Nq):
+        s = k[: n - Nq + i + 1, 0]
+        p = np.exp(s - s.max())
+        total = p.sum()
+        want = (p / total) @ v[: len(p)]
+        rel = 2.0 ** -11 + 2.0 ** -20 + n * 2.0 ** -24 + 4 * (D + 8) * 2.0 ** -24 * gap
+        tol = want * (rel + 2.0 ** -24) + n * 2.0 ** -32 * qmax / total
+        assert np.all(np.abs(o[i] - want) <= tol), (i, np.abs(o[i] / want - 1).max())
+        assert np.all(np.abs(lse[:, i] - (gap + math.log(total))) <= 2 * (D + 8) * 2.0 ** -24 * gap + 2.0 ** -20 + n * 2.0 ** -24)
