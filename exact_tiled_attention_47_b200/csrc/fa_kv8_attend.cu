@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
       }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += ex2(rm[w * kRows + tid] - M) * rl[w * kRows + tid];
-      const bool none = M == kNone;
+      const bool none = sum == 0.f;  // (not by M: scores of NaN leave that where it was)
       const float f = none ? 0.f : ex2(W + kHead) / sum;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) rw[w * kRows + tid] = ex2(rw[w * kRows + tid] - W) * f;

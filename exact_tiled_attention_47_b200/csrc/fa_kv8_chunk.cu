@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
       n0 += blocks;
       float l0, l1;
       f2_split(lsum, l0, l1);
-      const bool none = m == kNone;
+      const bool none = l0 + l1 == 0.f;  // (not by m: scores of NaN leave that where it was)
       const float f = none ? 0.f : ex2(mo - m + kHead) / (l0 + l1), ls = none ? -INFINITY : (m + lg2(l0 + l1)) * kLn2;
       const int slot = 2 * blockIdx.x + pc.slot;
       const size_t at = pc.whole ? o_row(p, pc.b, pc.hk, min(row, rows - 1)) : static_cast<size_t>(slot) * kUnitRows + t * kBM + r;

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(const AttP
   for (int i = 0; i < RPW; ++i) {
     const int row = part + (kMany ? 0 : warp) + i * kStride, rr = u.tile * kRows + row;
     if (row >= rows) continue;
-    const bool none = M[i] == kNone;
+    const bool none = sum[i] == 0.f;  // (not by M: a NaN leaves that where it was)
     const float inv = none ? 0.f : 1.f / sum[i];
     const size_t at = o_row(p, place.b, u.hk, rr);
     if (!idx_ok(p.status, at, 1, static_cast<long long>(p.B) * p.Nq * p.Hq)) continue;

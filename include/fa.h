@@ -311,7 +311,8 @@ size_t fa_kv8_attend_workspace_bytes(int B, int Nq, int Hq, int Hkv, int D);
  * NULL (pages_per_seq * page_size for every item): the queries are item b's last Nq keys' tokens, so
  * query i sees key j iff j <= seqlens_k[b] - Nq + i (the causal mask of fa_fwd, aligned at the
  * bottom-right corner).  A query that sees no key (a length below Nq, or 0) gets O = 0, LSE = -inf: in a
- * batch of chunks of unlike lengths the shorter ones are padded in front.  Rows of a page at or behind
+ * batch of chunks of unlike lengths the shorter ones are padded in front.  A NaN among a query's values makes
+ * O and LSE of that query NaN (if it sees a key) and of no other.  Rows of a page at or behind
  * seqlens_k[b] may hold anything, NaN codes included.  Among the keys below it a NaN code makes O
  * (V) or O and LSE (K) of any query of that item and head unspecified, masked from it or not
  * (fa_kv8_append writes none).  Scales are finite and not negative.

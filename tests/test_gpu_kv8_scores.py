@@ -106,3 +106,30 @@ def test_small_keys_beside_large_ones_of_no_value(case, kind, gap):
         tol = want * (rel + 2.0 ** -24) + n * 2.0 ** -32 * qmax / total
         assert np.all(np.abs(o[i] - want) <= tol), (i, np.abs(o[i] / want - 1).max())
         assert np.all(np.abs(lse[:, i] - (gap + math.log(total))) <= 2 * (D + 8) * 2.0 ** -24 * gap + 2.0 ** -20 + n * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_nan_in_a_query_stays_in_its_row(case, dtype):
+    n, Nq, G = case
+    rng = np.random.default_rng(n + 2)
+    k, v = (rng.integers(-7, 8, (n, D)).astype(np.float64) for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((Nq, G, D)) * 0.2).to(dtype)
+    clean_o, clean_lse = attend(q, k, v, 1.0, 1.0, "int8")
+    rows = [(0, 0), (Nq - 1, G - 1)]
+    for i, g in rows:
+        q[i, g, 5 + i % 50] = math.nan
+    o, lse = attend(q, k, v, 1.0, 1.0, "int8")
+    for i, g in rows:
+        assert np.isnan(o[i, g]).all() and np.isnan(lse[g, i]), (i, g, lse[g, i])
+        o[i, g], lse[g, i] = clean_o[i, g], clean_lse[g, i]
+    assert np.array_equal(o, clean_o) and np.array_equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("n,Nq,G", [(3, 5, 4), (40, 200, 2)])
+def test_a_nan_in_a_query_that_sees_no_key(n, Nq, G):
+    q = torch.full((Nq, G, D), math.nan, dtype=torch.bfloat16)
+    o, lse = attend(q, np.ones((n, D)), np.ones((n, D)), 1.0, 1.0, "e4m3")
+    dead = Nq - n
+    assert not o[:dead].any() and np.isneginf(lse[:, :dead]).all()
+    assert np.isnan(o[dead:]).all() and np.isnan(lse[:, dead:]).all()
