@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, NG>::kPerSm) kv8_attend_kern
       }
 
       const bool edge = key0 + kKv8Block > min(tile_all, hi);
-      const float lv = lg2(fmaxf(vs, 1.17549435e-38f));  // a scale of zero stands for values of zero
+      const float lv = log2_scale(vs);
       uint32_t wb[NG][2];
       float f[NG][2], mx[NG][2];
       bool past = false;

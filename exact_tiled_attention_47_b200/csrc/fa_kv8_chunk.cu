@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const __gri
           if (!ok) break;
         }
         store(sK + ks * C::kTileBytes, kx);
-        if (lane < 2) bars->scale[n & 3][cw * 2 + lane] = make_float2(sc.x, lg2(fmaxf(sc.y, 1.17549435e-38f)));
+        if (lane < 2) bars->scale[n & 3][cw * 2 + lane] = make_float2(sc.x, log2_scale(sc.y));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->k_full[ks]);

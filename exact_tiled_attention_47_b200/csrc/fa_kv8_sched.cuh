@@ -73,6 +73,9 @@ inline AttParams params_of(const Attend8Args& a) {
 // 2^e as fp32, e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// log2 of a V scale.  A scale of zero stands for values of zero: no weight, and no say in the maximum of O.
+__device__ __forceinline__ float log2_scale(float vs) { return vs > 0.f ? lg2(fmaxf(vs, 1.17549435e-38f)) : -INFINITY; }
+
 // Two weights as fp16.  Beyond scores of 10^7, where a step of the score is a factor of two and more, they could pass
 // its range: the largest finite value then.
 __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {

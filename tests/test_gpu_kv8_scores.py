@@ -133,3 +133,22 @@ def test_a_nan_in_a_query_that_sees_no_key(n, Nq, G):
     dead = Nq - n
     assert not o[:dead].any() and np.isneginf(lse[:, :dead]).all()
     assert np.isnan(o[dead:]).all() and np.isnan(lse[:, dead:]).all()
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_v_scales_of_zero_stand_for_zeros(case):
+    # codes under a scale of zero: 0 exactly where there is nothing else, and as if the codes were zeros beside other blocks
+    n, Nq, G = case
+    rng = np.random.default_rng(n + 3)
+    k, v = (rng.integers(-7, 8, (n, D)).astype(np.float64) for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((Nq, G, D)) * 0.2).to(torch.bfloat16)
+    o, lse = attend(q, k, v, 1.0, 0.0, "int8")
+    same_o, same_lse = attend(q, k, np.zeros((n, D)), 1.0, 1.0, "int8")
+    assert not o.any() and not same_o.any()
+    assert np.all(np.abs(lse - same_lse) <= 2.0 ** -20 + n * 2.0 ** -24)  # (the sums may be added up in another way)
+    some = np.arange(-(-n // 16)) % 3 > 0
+    o, lse = attend(q, k, v, 1.0, np.where(some, 1.0, 0.0), "int8")
+    want, want_lse = attend(q, k, v * np.repeat(some, 16)[:n, None], 1.0, 1.0, "int8")
+    # two roundings of each weight to fp16 (2^-11 of the values added up, or 2^-32 of the largest) apart
+    p = 2.0 ** -10 * np.abs(v).max() + n * 2.0 ** -31 * 7
+    assert np.all(np.abs(o - want) <= p) and np.all(np.abs(lse - want_lse) <= 2.0 ** -20 + n * 2.0 ** -24)
