@@ -156,21 +156,24 @@ __device__ __forceinline__ void weights32(const uint32_t (&sr)[64], int ch, uint
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const float2 sc = scale_at(scale, h);
-    const float f = fmaxf(qs * sc.x, 1.17549435e-38f), e = sc.y - mo;
-    const float d = kOwnSum ? 1.f : ex2(mo - m - sc.y);
-    const uint64_t f2v = f2(f, f), e2v = f2(e, e), d2v = f2(d, d), m2v = f2(-m, -m);
+    const float f = fmaxf(qs * sc.x, 1.17549435e-38f), e = kOwnSum ? -m : sc.y - mo;
+    const float d = kOwnSum ? sc.y - (mo - m) : ex2(mo - m - sc.y);
+    const uint64_t f2v = f2(f, f), e2v = f2(e, e), d2v = f2(d, d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = ch * 32 + h * 16 + 2 * i;
       const uint64_t s2 = f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-      const uint64_t x = f2_fma(s2, f2v, e2v);
+      uint64_t x = f2_fma(s2, f2v, e2v);
       float x0, x1;
+      if constexpr (kOwnSum) {  // the weight from the s f - m of the row sum: rounded once, at the size of the score
+        f2_split(x, x0, x1);
+        acc0 = f2_add(acc0, f2(ex2(x0), ex2(x1)));
+        x = f2_add(x, d2v);
+      }
       f2_split(x, x0, x1);
       const float p0 = ex2(x0), p1 = ex2(x1);
       const uint64_t pe = f2(p0, p1);
       if constexpr (kOwnSum) {
-        f2_split(f2_fma(s2, f2v, m2v), x0, x1);
-        acc0 = f2_add(acc0, f2(ex2(x0), ex2(x1)));
       } else if (i & 1) {
         acc1 = f2_fma(pe, d2v, acc1);
       } else {

@@ -152,3 +152,21 @@ def test_v_scales_of_zero_stand_for_zeros(case):
     # two roundings of each weight to fp16 (2^-11 of the values added up, or 2^-32 of the largest) apart
     p = 2.0 ** -10 * np.abs(v).max() + n * 2.0 ** -31 * 7
     assert np.all(np.abs(o - want) <= p) and np.all(np.abs(lse - want_lse) <= 2.0 ** -20 + n * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+@pytest.mark.parametrize("score", [1e5, 1e6])
+def test_one_key_far_ahead_beside_blocks_of_small_values(case, score):
+    # as test_one_key_far_ahead_at_large_scores, with V scales of 2^-100 in every other block (what an append of zeros leaves)
+    n, Nq, G = case
+    rng = np.random.default_rng(n)
+    k = np.zeros((n, D))
+    k[:, 0], k[5, 0] = 60.0, 120.0
+    v = rng.integers(1, 8, (n, D)).astype(np.float64)
+    q = torch.zeros((Nq, G, D), dtype=torch.float16)
+    q[..., 0] = 1.0
+    scale = float(np.float32(score / 120.0 * 1.0314159))
+    o, lse = attend(q, k, v, 1.0, np.where(np.arange(-(-n // 16)) % 2, 2.0 ** -100, 0.37), "int8", scale)
+    want = v[5] * float(np.float32(0.37))
+    assert np.all(np.abs(o - want) <= want * (2.0 ** -11 + 2.0 ** -18)), np.abs(o / want - 1).max()
+    assert np.all(np.abs(lse - 120.0 * scale) <= 2.0 ** -21 * 120.0 * scale)
