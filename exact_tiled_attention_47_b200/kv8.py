@@ -67,28 +67,32 @@ def fa_kv8_attend(q, k_pages, v_pages, k_scales, v_scales, block_table, o, lse, 
                                 floats.get(o.dtype, -1) if o_dtype is None else int(o_dtype))
 
 
-def enter(device, stream):
-    """(context, raw stream) of a helper's call on tensors of this device: the context makes their device and
-    the caller's stream current, so that what the helper allocates belongs to the stream its kernels run on;
-    it is None where both already are."""
+@contextlib.contextmanager
+def _on(device, stream):
+    with _TORCH.cuda.device(device), contextlib.nullcontext() if stream is None else _TORCH.cuda.stream(stream):
+        yield
+
+
+def place_of(device, stream):
+    """(context, raw stream) of a helper's call on tensors of this device: entered (in_context), the context makes their
+    device and the caller's stream current, so that what the helper allocates belongs to the stream its kernels run on;
+    it is None where both already are.  Nothing is entered here: a helper may still return or refuse."""
     if stream is None and device.type == "cuda" and device.index == _torch().cuda.current_device():
         return None, _TORCH._C._cuda_getCurrentRawStream(device.index)
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    torch = _TORCH
-    stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-        if stream.device != device:
-            raise ValueError("the stream belongs to another device than the tensors")
-        stack.enter_context(torch.cuda.stream(stream))
-    return stack, torch.cuda.current_stream(device).cuda_stream
+    cuda = _TORCH.cuda
+    if stream is None:
+        return _on(device, None), cuda.current_stream(device).cuda_stream
+    if isinstance(stream, int):
+        stream = cuda.ExternalStream(stream, device=device) if stream else cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return _on(device, stream), stream.cuda_stream
 
 
 def in_context(context, f, *args):
-    """f(*args) inside a context of enter()."""
+    """f(*args) inside a context of place_of()."""
     if context is None:
         return f(*args)
     with context:
@@ -158,7 +162,7 @@ def append_kv8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_
         check_tensor("new_lens", new_lens, _INT32, (B,), dev)
     if v.dtype is not dtype or v.shape != shape or v.device != dev:
         raise ValueError("k and v must be alike")
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
     if context is not None or not (k.is_contiguous() and v.is_contiguous()):
         with context or contextlib.nullcontext():
             k, v = k.contiguous(), v.contiguous()
@@ -190,7 +194,7 @@ def attend_kv8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k=N
     num_pages, Hkv, page_size, pps, code = _check_cache(k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, B, None, D, dev)
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace: expected a contiguous tensor on the device of q")
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
 
     def call():
         rq = q if q.is_contiguous() else q.contiguous()

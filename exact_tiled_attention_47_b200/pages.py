@@ -15,7 +15,7 @@ import exact_tiled_attention_47_b200 as fa
 
 from . import _lib, kv8
 from ._lib import load
-from .kv8 import alike, check_tensor, enter, in_context
+from .kv8 import alike, check_tensor, in_context, place_of
 
 
 def _pointers(pools):
@@ -139,7 +139,7 @@ def extend_pages(block_table, seqlens, refcount, page_size, add, slots=None, wor
     if slots is not None:
         _check_list("slots", slots, n, dev)
     _check_workspace(workspace, dev)
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
     if n == 0:
         return
 
@@ -159,7 +159,7 @@ def fork_pages(block_table, seqlens, refcount, page_size, src, dst, pools, works
     _check_list("dst", dst, n, dev)
     sizes = _page_bytes(pools, num_pages, dev)
     _check_workspace(workspace, dev)
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
     if n == 0:
         return
 
@@ -176,7 +176,7 @@ def free_pages(block_table, seqlens, refcount, page_size, slots, stream=None):
     """Empty slots (int32 [n]) and give back the pages that nobody else holds."""
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     n = _check_list("slots", slots, None, dev)
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
     if n == 0:
         return
 
@@ -196,7 +196,7 @@ def compact_pages(block_table, seqlens, refcount, page_size, pools, in_place=Fal
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     sizes = _page_bytes(pools, num_pages, dev)
     _check_workspace(workspace, dev)
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
 
     def call():
         like = kv8._TORCH.empty_like
@@ -225,7 +225,7 @@ def copy_pages(src_pools, dst_pools, src, dst, workspace=None, stream=None):
     if sizes != _page_bytes(dst_pools, b, dev):
         raise ValueError("source and destination pools have pages of unlike sizes")
     _check_workspace(workspace, dev)
-    context, raw = enter(dev, stream)
+    context, raw = place_of(dev, stream)
     if n == 0:
         return
 
