@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PlanParam
         else need = len % p.page_size ? 1 : 0;
         if (need) {
           const int page = p.table[static_cast<long long>(src) * p.pps + len / p.page_size];
-          if (page < 0 || page >= p.num_pages) bad = max(bad, kStatusPageTable);
+          if (page < 0 || page >= p.num_pages || p.refs[page] <= 0) bad = max(bad, kStatusPageTable);
         }
       }
     }
@@ -240,6 +240,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PlanParam
   }
   if (!accept(p, bad, &s_bad)) return;
   if (!accept(p, take_free(p, total, p.w.pdst, cnt, sums) ? 0 : kStatusNoPages, &s_bad)) return;
+  // the pages handed out, found again by page (the marks of the slots are done with): see fork_kernel
+  for (int j = tid; j < total; j += kPlanThreads) p.w.mark[p.w.pdst[j]] = j;
   for (int i = tid; i < p.n; i += kPlanThreads) {
     const int src = p.a[i], dst = p.b[i], len = p.seqlens[src];
     if (len % p.page_size) {
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 }
 
 // Fork: the first p.n CTAs write the destinations' table rows and count the shared pages, the others
-// copy the last partial pages.
+// copy the last partial pages.  A page of the source that is not in the pool or that nobody holds is not shared: its
+// count is 0 (held pages are at 1 or more throughout), or this very call has handed it out.
 __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constant__ MoveParams m, const PlanParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
   if (m.head[1] == 0) return;
@@ -412,12 +415,17 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
     return;
   }
   const int src = p.a[blockIdx.x], dst = p.b[blockIdx.x];
-  const int full = p.seqlens[src] / p.page_size;
+  const int full = p.seqlens[src] / p.page_size, handed = m.head[0];
   for (int c = threadIdx.x; c < full; c += kMoveThreads) {
     const int page = p.table[static_cast<long long>(src) * p.pps + c];
-    p.table[static_cast<long long>(dst) * p.pps + c] = page;
-    if (page < 0 || page >= p.num_pages) record_status(p.status, kStatusPageTable);
-    else atomicAdd(p.refs + page, 1);
+    bool held = page >= 0 && page < p.num_pages;
+    if (held) {
+      const int count = p.refs[page], j = p.w.mark[page];  // (the mark is any number where the page was not handed out)
+      held = count > 0 && (j < 0 || j >= handed || m.pdst[j] != page);
+    }
+    p.table[static_cast<long long>(dst) * p.pps + c] = held ? page : -1;
+    if (held) atomicAdd(p.refs + page, 1);
+    else record_status(p.status, kStatusPageTable);
   }
 }
 

@@ -375,7 +375,8 @@ int fa_pages_extend(int* block_table, int* seqlens, int* refcount, const int* sl
  * last partial page is copied in every pool to a free page, so that both may go on on their own.
  * A source may be named several times; the destinations are distinct, empty (length 0) and no sources.
  * On the device: FA_ERR_SLOTS, FA_ERR_CU_SEQLENS, FA_ERR_NO_PAGES, FA_ERR_PAGE_TABLE for a partial page
- * outside the pool (nothing changed), and FA_ERR_PAGE_TABLE for a full page outside it (not counted).
+ * outside the pool or held by nobody (nothing changed), and FA_ERR_PAGE_TABLE for such a full page (its entry of the
+ * copy becomes -1, the rest of the request is met).
  */
 int fa_pages_fork(int* block_table, int* seqlens, int* refcount, const int* src, const int* dst, int n, int S,
                   int pages_per_seq, int num_pages, int page_size, void* const* pools, const size_t* page_bytes,
