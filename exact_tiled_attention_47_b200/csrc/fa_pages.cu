@@ -329,10 +329,12 @@ __global__ void __launch_bounds__(256) free_kernel(const PlanParams p) {
     return;
   }
   if (threadIdx.x == 0) {
-    int len = atomicExch(p.seqlens + s, 0);  // a slot that is named twice is freed by whoever comes first
-    if (len < 0 || len > capacity(p)) {
+    int len = p.seqlens[s];
+    if (len < 0 || len > capacity(p)) {  // its pages cannot be told: the slot stays as it is
       record_status(p.status, kStatusCuSeqlens);
       len = 0;
+    } else if (atomicCAS(p.seqlens + s, len, 0) != len) {
+      len = 0;  // a slot that is named twice is freed by whoever comes first
     }
     s_len = len;
   }

@@ -384,8 +384,9 @@ int fa_pages_fork(int* block_table, int* seqlens, int* refcount, const int* src,
 
 /*
  * fa_pages_free -- empty slots: their pages' counts fall by one, their used table entries become -1,
- * their lengths 0.  An empty slot, or a slot named again, is left as it is.  On the device: FA_ERR_SLOTS,
- * FA_ERR_CU_SEQLENS, FA_ERR_PAGE_TABLE (an entry outside the pool, or of a page nobody holds).
+ * their lengths 0.  An empty slot, or a slot named again, is left as it is.  On the device (each slot by itself: the
+ * others of the request are freed): FA_ERR_SLOTS, FA_ERR_CU_SEQLENS (the slot is left as it is, its length too),
+ * FA_ERR_PAGE_TABLE (an entry outside the pool, or of a page nobody holds: passed over).
  */
 int fa_pages_free(int* block_table, int* seqlens, int* refcount, const int* slots, int n, int S,
                   int pages_per_seq, int num_pages, int page_size, fa_stream_t stream);

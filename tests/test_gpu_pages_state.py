@@ -59,3 +59,20 @@ def test_fork_of_a_full_page_that_nobody_holds(bad, forks):
     assert all(torch.equal(x[8], x[7]) for x in t.gp)
     assert t.gr.tolist() == [1 + forks, 1 + forks, 1, 1 + forks, 2, 2, 2, 1, 1] + [0] * 7
     assert t.gl.tolist() == [64, 50] + [64] * forks + [0] * (8 - forks) + [50, 0]
+
+
+@pytest.mark.parametrize("length", [-1, 65, 2 ** 31 - 1, -2 ** 31])
+def test_free_of_a_slot_whose_length_is_out_of_range(length):
+    import exact_tiled_attention_47_b200 as fa
+    t = Both(3, 4, 4, 16, 16)
+    assert t.extend([0, 1, 2], [40, 33, 64])
+    t.lens[1] = length
+    t.dev()
+    fa.free_pages(t.gt, t.gl, t.gr, 16, i32([0, 1, 1, 2]))
+    assert status() == fa.FA_ERR_CU_SEQLENS
+    # slots 0 and 2 are free, slot 1 is as it was: put right, it can be freed as well
+    assert t.gl.tolist() == [0, length, 0, 0] and t.gr.tolist() == [0, 0, 0, 1, 1, 1] + [0] * 10
+    assert t.gt[1].tolist() == t.table[1].tolist() and (t.gt[[0, 2]] == -1).all()
+    t.gl[1] = 33
+    fa.free_pages(t.gt, t.gl, t.gr, 16, i32([1, 1]))
+    assert status() == 0 and not t.gl.any() and not t.gr.any()
