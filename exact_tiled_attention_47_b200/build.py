@@ -50,8 +50,10 @@ def _headers():
 
 # Kernels whose warpgroups re-split their registers with setmaxnreg: the split only works when the
 # kernel is launched with exactly the register count the source plans for (kLaunchRegs), so the
-# build fails if ptxas allocated anything else or spilled.
-REGISTER_PLANNED = {"fa_prefill_sm100.cu": ("fa_fwd_kernel", "kLaunchRegs")}
+# build fails if ptxas allocated anything else, or spilled where the source plans without spills (the
+# 8-bit cache's chunk kernel keeps a few bytes in local memory: that costs no more than time).
+REGISTER_PLANNED = {"fa_prefill_sm100.cu": ("fa_fwd_kernel", "kLaunchRegs", False),
+                    "fa_kv8_chunk.cu": ("kv8_chunk_kernel", "kLaunchRegs", True)}
 
 
 def ptxas_kernels(report: str):
@@ -78,7 +80,7 @@ def check_planned_registers(src_name: str, source: str, report: str) -> None:
     """Raise RuntimeError unless every planned kernel of the file got exactly its planned registers."""
     if src_name not in REGISTER_PLANNED:
         return
-    kernel, const = REGISTER_PLANNED[src_name]
+    kernel, const, may_spill = REGISTER_PLANNED[src_name]
     m = re.search(r"constexpr int " + const + r" = (\d+);", source)
     if not m:
         raise RuntimeError(f"{src_name}: no '{const}' constant found")
@@ -86,9 +88,9 @@ def check_planned_registers(src_name: str, source: str, report: str) -> None:
     found = {k: v for k, v in ptxas_kernels(report).items() if kernel in k}
     if not found:
         raise RuntimeError(f"{src_name}: ptxas reported no {kernel} instantiation")
-    bad = {k: v for k, v in found.items() if v[0] != planned or v[1] != 0}
+    bad = {k: v for k, v in found.items() if v[0] != planned or (v[1] != 0 and not may_spill)}
     if bad:
-        raise RuntimeError(f"{src_name}: {kernel} must use exactly {planned} registers without spills "
+        raise RuntimeError(f"{src_name}: {kernel} must use exactly {planned} registers{'' if may_spill else ' without spills'} "
                            f"(setmaxnreg split); ptxas gave {sorted(set(bad.values()))}")
 
 
