@@ -133,7 +133,11 @@ def _raise(st, where):
 
 
 def extend_pages(block_table, seqlens, refcount, page_size, add, slots=None, workspace=None, stream=None):
-    """Lengthen slots (int32 [n]; None: the first n) by ``add`` (int32 [n]) keys each, with the pages that takes."""
+    """Lengthen slots (int32 [n]; None: the first n) by ``add`` (int32 [n], not negative) keys each, with the pages that takes.
+
+    To take keys back (rejected drafts), keep ``seqlens`` as what the slots hold and pass ``append_kv8`` and ``attend_kv8``
+    valid lengths of their own; or lower ``seqlens`` inside a slot's last page.  Lowered past a page's border, pages are lost.
+    """
     S, pps, num_pages, dev = _check_state(block_table, seqlens, refcount)
     n = _check_list("add", add, None, dev)
     if slots is not None:

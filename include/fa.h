@@ -364,6 +364,13 @@ size_t fa_pages_workspace_bytes(int n, int S, int num_pages);
  * slots: the slots to lengthen, each at most once, or NULL (slots 0 .. n - 1; n <= S).  add[i] >= 0 and
  * the new length at most pages_per_seq * page_size.  seqlens, block_table and refcount are updated.  The
  * last page of a slot must not be shared if it is partial (fa_pages_fork sees to that).
+ * Slots only grow: to take keys back (drafted tokens that were not accepted) is the caller's, in one of two ways.
+ * (a) Lower seqlens[s], but never past the border of a page: ceil(seqlens[s] / page_size) is what the slot holds, and a
+ * page beyond it stays counted for good (free and fork do not look there, the next extend writes over its entry).
+ * (b) Leave seqlens as what the slot holds, pass the valid lengths, at most as long, to fa_kv8_append and
+ * fa_kv8_attend in an array of their own, and extend by what the next step lacks (or by 0).  Before such a slot is
+ * forked, its valid length must reach at least into its last page (valid >= seqlens[s] / page_size * page_size, rounded
+ * down): a full page is shared, so nothing may be appended to it any more.
  * On the device: FA_ERR_SLOTS, FA_ERR_CU_SEQLENS, FA_ERR_NO_PAGES (nothing changed).
  */
 int fa_pages_extend(int* block_table, int* seqlens, int* refcount, const int* slots, const int* add, int n,
