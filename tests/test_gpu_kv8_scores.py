@@ -170,3 +170,41 @@ def test_one_key_far_ahead_beside_blocks_of_small_values(case, score):
     want = v[5] * float(np.float32(0.37))
     assert np.all(np.abs(o - want) <= want * (2.0 ** -11 + 2.0 ** -18)), np.abs(o / want - 1).max()
     assert np.all(np.abs(lse - 120.0 * scale) <= 2.0 ** -21 * 120.0 * scale)
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+@pytest.mark.parametrize("step", [0.3, 5.0, 5.6, 40.0, -5.0])  # nats from one block to the next; the lazy maxima move from 5.5 on
+@pytest.mark.parametrize("values", ["even", "rising", "falling", "mixed"])
+def test_scores_and_scales_that_climb(case, step, values):
+    # K has the same codes everywhere and a scale that grows from block to block, so scores climb by `step`; V scales stay, climb
+    # or fall by 2^3 a block (for 40 blocks, then again), or jump about: both maxima are raised late, early and apart.
+    n, Nq, G = case
+    rng = np.random.default_rng(n + 4)
+    blocks = -(-n // 16)
+    at = np.arange(blocks)
+    ks = np.abs(step) / 8 * (at % 50 + 1 if step > 0 else 50 - at % 50)
+    vs = {"even": np.ones(blocks), "rising": 2.0 ** (3 * (at % 40) - 60), "falling": 2.0 ** (60 - 3 * (at % 40)),
+          "mixed": 2.0 ** rng.integers(-40, 40, blocks)}[values]
+    ks = ks.astype(np.float32).astype(np.float64)
+    k = np.zeros((n, D))
+    k[:, 0] = 8.0 + rng.integers(0, 2, n)
+    v = rng.integers(-7, 8, (n, D)).astype(np.float64)
+    q = torch.zeros((Nq, G, D), dtype=torch.bfloat16)
+    q[..., 0] = torch.arange(1, G + 1) / 4
+    scale = 4.0 / G
+    o, lse = attend(q, k, v, ks, vs, "int8", scale)
+    per_key_k, per_key_v = np.repeat(ks, 16)[:n], np.repeat(vs, 16)[:n]
+    for i in sorted({0, Nq // 2, Nq - 1}):
+        vis = n - Nq + i + 1
+        for g in range(G):
+            s = np.float64(np.float32(scale)) * (g + 1) / 4 * (k[:vis, 0] * per_key_k[:vis])
+            p = np.exp(s - s.max())
+            total = p.sum()
+            p /= total
+            V = v[:vis] * per_key_v[:vis, None]
+            want, spread = p @ V, p @ np.abs(V)
+            ds = 16 * 2.0 ** -24 * s.max()  # one product and a handful of roundings at the size of the score
+            rel = 2.0 ** -11 + 2 * ds + 2.0 ** -18 + n * 2.0 ** -24
+            tol = spread * rel + n * 2.0 ** -32 * 7 * (p * per_key_v[:vis]).max() + np.abs(want) * 2.0 ** -23
+            assert np.all(np.abs(o[i, g] - want) <= tol), (i, g, (np.abs(o[i, g] - want) / tol).max())
+            assert abs(lse[g, i] - (s.max() + math.log(total))) <= ds + 2.0 ** -18 + n * 2.0 ** -24
