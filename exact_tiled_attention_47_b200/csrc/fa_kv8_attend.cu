@@ -31,10 +31,11 @@
 // MMA a value takes is free as long as both operands agree, so no transposition is needed but of the
 // byte pairs of V (two PRMT per eight codes).  The ring's 16-byte chunks are swizzled so that both reads
 // are free of bank conflicts.  Warps and pieces are merged by their (m, l, mo, O).
-// What bounds it: up to 16 rows the reads (4 x 131072 keys, 32 heads, int8: 176 us, 6.1 TB/s, e4m3 185; without
+// What bounds it: up to 16 rows the reads (4 x 131072 keys, 32 heads, int8: 178 us, 6.0 TB/s, e4m3 182; without
 // any arithmetic 164 us), above that the instructions of two warps per scheduler, which depend on one another from the first
-// product over the softmax to the second (24 rows: 430 instructions a block of 16 keys in 1170 cycles; neither
-// fewer matrix products nor fewer conversions or exponentials make it shorter).
+// product over the softmax to the second (24 rows: about 430 instructions for a block of 16 keys, one every 1170 cycles
+// on a scheduler, so 2340 for each of its two warps; neither fewer matrix products nor fewer conversions or exponentials
+// make it shorter).
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -54,7 +55,7 @@ constexpr int kWholeKeys = 1024;  // tables up to this many keys: a granule is a
 constexpr int kManyPieces = 16;  // CTAs per unit from which on tiles of up to 16 rows are merged by many CTAs (32: 4 x 32768 keys,
                                  // 4 heads 37 us where 16 takes 34; 24 rows, 8 x 20221: 39 us with them, 33 without)
 constexpr int kWarpRows = 64;  // more rows per KV head than this take the tcgen05 kernel (B8, 8 KV heads, D 128; 40 rows,
-                               // 8192 keys: 83 us here, 106 there; 64, 4096: 64 and 67; 96, 2048: 58 and 51)
+                               // 8192 keys: 85 us here, 107 there; 64, 4096: 65 and 67; 96, 2048: 58 and 52)
 
 // CTAs per SM for tiles of NG * 8 rows (O takes 32 registers per eight rows at D = 128), and the ring.  Four of
 // one group left 128 registers and less overlap inside a warp: 200 us where three took 193 (4 x 131072, int8).

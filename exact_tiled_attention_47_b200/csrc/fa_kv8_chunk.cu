@@ -19,7 +19,7 @@
 // Tensor memory: S0 S1 [0, 256), O0 O1 [256, 256 + 2 D).  Warps 0-3 and 4-7: softmax of tile 0 and 1; 8 and 9: MMA
 // issue (10 and 11 idle); 12-15: conversion.  16 warps share the registers, so a row of S is never held as a whole: its
 // two halves are read for the maxima, the second is turned into weights and stored, the first is read again.
-// A step of 128 keys takes 5660 cycles (1024 tokens behind 15360 cached keys, two sequences: 700 us, 761 TFLOP/s), of
+// A step of 128 keys takes about 5800 cycles (1024 tokens behind 15360 cached keys, two sequences: 718 us, 742 TFLOP/s), of
 // which the MUFU needs 2180 and the tensor core 2100: what is left is latency inside the softmax warps, of which the
 // registers allow two per scheduler.
 #include <algorithm>

@@ -320,7 +320,8 @@ size_t fa_kv8_attend_workspace_bytes(int B, int Nq, int Hq, int Hkv, int D);
  * weights are rounded to fp16, relative to the row's largest contribution to O (weight times V scale): to 11
  * bits down to 2^-21 of it and to steps of 2^-31 of it below, so that a key below 2^-32 of it adds nothing to O
  * (its weight stays in the sum and in LSE).  With o_dtype FA_FP32 that rounding is what O is exact to.
- * Nothing else is rounded below fp32 before O.  Nq * Hq * B and B * Hkv * Nq below 2^31; Nq at most 2^24.
+ * Nothing else is rounded below fp32 before O.  Scores (scale q.K) are fp32: up to 2^26 in magnitude O is as exact as
+ * that; a step of a larger one is a factor of 2^8 and more, and O and LSE of such a row are unspecified.  Nq * Hq * B and B * Hkv * Nq below 2^31; Nq at most 2^24.
  * workspace: at least fa_kv8_attend_workspace_bytes(B, Nq, Hq, Hkv, D) bytes, 16-byte aligned, owned by the
  * caller; its contents on entry are irrelevant; calls that may overlap need one each.
  * Errors as above, plus FA_ERR_WORKSPACE.

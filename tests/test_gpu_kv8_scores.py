@@ -57,7 +57,7 @@ def attend(q, k, v, ks, vs, kind, scale=None):
 
 @pytest.mark.parametrize("case", CASES, ids=IDS)
 @pytest.mark.parametrize("kind", list(CODE))
-@pytest.mark.parametrize("score", [1e3, 1e5, 1e6])
+@pytest.mark.parametrize("score", [1e3, 1e5, 1e6, 5e7])
 def test_one_key_far_ahead_at_large_scores(case, kind, score):
     # Key 5 has the score given, every other one half of it: the softmax is 1 at key 5 and 0 elsewhere, so O is that key's
     # value.  Its weight is off by 2^-11 (rounded to fp16) and by the exponentials and the merges (2^-22 each, a handful,
@@ -155,7 +155,7 @@ def test_v_scales_of_zero_stand_for_zeros(case):
 
 
 @pytest.mark.parametrize("case", CASES, ids=IDS)
-@pytest.mark.parametrize("score", [1e5, 1e6])
+@pytest.mark.parametrize("score", [1e5, 1e6, 5e7])
 def test_one_key_far_ahead_beside_blocks_of_small_values(case, score):
     # as test_one_key_far_ahead_at_large_scores, with V scales of 2^-100 in every other block (what an append of zeros leaves)
     n, Nq, G = case
