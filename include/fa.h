@@ -342,7 +342,8 @@ int fa_kv8_attend(const void* q, const void* k_pages, const void* v_pages, const
  * ceil(seqlens[s] / page_size) entries of a row are in use, the others mean nothing.
  * Pages are handed out from the lowest free one on, in the order of the request's list, so the outcome
  * depends on the inputs alone.  A request of fa_pages_extend, _fork or _copy is met as a whole or, when the
- * device finds it faulty, changes nothing and sets the device status.
+ * device finds it faulty, changes nothing and sets the device status (a full page of a fork that is not held is the
+ * exception: see there).
  * Slot, page and length lists (slots, add, src, dst) are device int32 of n entries, 4-byte aligned.
  * page_size as above; S, n, num_pages, pages_per_seq >= 1; S * pages_per_seq below 2^31,
  * pages_per_seq * page_size at most 2^30, n at most 2^20, num_pages and S at most 2^28.
